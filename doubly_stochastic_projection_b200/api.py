@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -68,6 +69,16 @@ def lib() -> ctypes.CDLL:
                 "mhc_mix_post_bwd": [p, p, p, p, p, i64, i64, p],
                 "mhc_mix_premap_bwd": [p, p, p, p, p, p, p, p, p, i64, i64, p],
                 "mhc_composite_gain": [p, p, p, p, i64, i64, p],
+                "mhc_mx_pack": [p, p, p, i64, i64, i32, p],
+                "mhc_mx_unpack": [p, p, p, i64, i64, i32, p],
+                "mhc_residual_mix_fwd_ckpt": [p] * 9 + [i64, i64, i32, p],
+                "mhc_proj_mix_fwd_ckpt": [p] * 10 + [i64, i64, i32, i32, p],
+                "mhc_residual_mix_bwd_ckpt": [p] * 12 + [i64, i64, i32, p],
+                "mhc_mix_post_bwd_ckpt": [p] * 6 + [i64, i64, i32, p],
+                "mhc_mix_premap_bwd_ckpt": [p] * 10 + [i64, i64, i32, p],
+                "mhc_premap_fwd_mx4": [p, p, p, p, i64, i64, p],
+                "mhc_mx4_linear": [p, p, p, p, p, i64, i64, i64, p],
+                "mhc_mx4_linear_mix": [p, p, p, p, p, p, p, p, i64, i64, i64, p],
                 "mhc_residual_mix_fwd": [p, p, p, p, p, i64, i64, p],
                 "mhc_residual_mix_bwd": [p, p, p, p, p, p, p, p, p, p, i64, i64, p],
                 "mhc_proj_mix_fwd": [p, p, p, p, p, p, i64, i64, i32, p],
@@ -453,6 +464,260 @@ def composite_gain(P_layers, need_M=True):
     return M, gr, gc
 
 
+MX_INT8 = 0
+MX_E4M3 = 1
+MX_E2M1 = 2
+_MX_FORMATS = {"int8": MX_INT8, "e4m3": MX_E4M3, "e2m1": MX_E2M1}
+
+
+class MxTensor(NamedTuple):
+    """A microscaled tensor [..., C]: blocks of 32 channels that share one
+    power-of-two scale.
+
+    ``codes``: uint8 [..., C] ("int8", "e4m3") or [..., C / 2] ("e2m1", the even
+    channel in the low half); ``scales``: uint8 [..., mx_scale_pitch(C)], a
+    block's exponent + 127, zero bytes up to a multiple of four; ``fmt``: the
+    format's name."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    fmt: str
+
+    @property
+    def shape(self):
+        """Shape of the tensor that the codes stand for."""
+        s = self.codes.shape
+        return s[:-1] + (s[-1] * 2,) if self.fmt == "e2m1" else s
+
+
+def mx_scale_pitch(C: int) -> int:
+    """Bytes of one row of scales for rows of C channels."""
+    return 4 * ((C + 127) // 128)
+
+
+def _mx_format(fmt, allowed=("int8", "e4m3", "e2m1")):
+    if fmt not in allowed:
+        raise ValueError("format must be one of %s, got %r" % (", ".join(allowed), fmt))
+    return _MX_FORMATS[fmt]
+
+
+def _mx_empty(shape, fmt, device):
+    C = shape[-1]
+    codes = torch.empty(shape[:-1] + ((C // 2) if fmt == "e2m1" else C,), dtype=torch.uint8, device=device)
+    return MxTensor(codes, torch.empty(shape[:-1] + (mx_scale_pitch(C),), dtype=torch.uint8, device=device), fmt)
+
+
+def _need_mx(mx, name, allowed, shape=None):
+    """Checks a MxTensor and returns the shape that it stands for."""
+    if not isinstance(mx, MxTensor):
+        raise TypeError("%s must be an MxTensor" % name)
+    _mx_format(mx.fmt, allowed)
+    _need(mx.codes, name + ".codes", torch.uint8)
+    if mx.codes.dim() < 1:
+        raise ValueError("%s.codes must have at least one dimension" % name)
+    s = tuple(mx.shape)
+    if shape is not None and s != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), s))
+    _need(mx.scales, name + ".scales", torch.uint8, s[:-1] + (mx_scale_pitch(s[-1]),))
+    return s
+
+
+_CKPT_FORMATS = ("int8", "e4m3")
+
+
+def _launch(f, *args):
+    """Calls entry point f on the current stream of its tensors' device, which must
+    be one and the same; the device is made current for the launch."""
+    dev = None
+    ptrs = []
+    for a in args:
+        if isinstance(a, torch.Tensor):
+            if dev is None:
+                dev = a.device
+            elif a.device != dev:
+                raise ValueError("tensors are on %s and %s" % (dev, a.device))
+            ptrs.append(a.data_ptr())
+        else:
+            ptrs.append(a)
+    if dev.index == torch.cuda.current_device():
+        rc = f(*ptrs, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*ptrs, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != 0:
+        _check(rc)
+
+
+def mx_pack(x, fmt, out: MxTensor | None = None) -> MxTensor:
+    """Microscaled codes of a bf16 tensor [..., C] (``fmt``: "int8", "e4m3" or
+    "e2m1").  Restored values differ from x by at most half a step of the
+    element type at the block's scale; a block with an infinity or NaN
+    restores as NaN."""
+    _need(x, "x", torch.bfloat16)
+    f = _mx_format(fmt)
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    shape = tuple(x.shape)
+    C = shape[-1]
+    if out is None:
+        out = _mx_empty(shape, fmt, x.device)
+    else:
+        _need_mx(out, "out", (fmt,), shape)
+    _launch(lib().mhc_mx_pack, x, out.codes, out.scales, x.numel() // C if C else 0, C, f)
+    return out
+
+
+def mx_unpack(mx: MxTensor, out=None):
+    """The bf16 tensor that a microscaled tensor stands for (exact in bf16)."""
+    shape = _need_mx(mx, "mx", tuple(_MX_FORMATS))
+    C = shape[-1]
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=mx.codes.device)
+    _need(out, "out", torch.bfloat16, shape)
+    _launch(lib().mhc_mx_unpack, mx.codes, mx.scales, out, out.numel() // C if C else 0, C, _MX_FORMATS[mx.fmt])
+    return out
+
+
+def residual_mix_fwd_ckpt(X, H_res, h_post, F, fmt="int8", out=None):
+    """residual_mix_fwd that also writes the 8-bit checkpoints ("int8" or "e4m3")
+    of X and F for the backward.  Returns (Y, Xq, Fq)."""
+    T, C = _mix_shapes(X, F)
+    f = _mx_format(fmt, _CKPT_FORMATS)
+    _need(H_res, "H_res", torch.float32, (T, 4, 4))
+    _need(h_post, "h_post", torch.float32, (T, 4))
+    Y = torch.empty_like(X) if out is None else _need(out, "out", torch.bfloat16, X.shape)
+    Xq, Fq = _mx_empty((T, 4, C), fmt, X.device), _mx_empty((T, C), fmt, X.device)
+    _launch(lib().mhc_residual_mix_fwd_ckpt, X, H_res, h_post, F, Y, Xq.codes, Xq.scales, Fq.codes, Fq.scales, T, C, f)
+    return Y, Xq, Fq
+
+
+def proj_mix_fwd_ckpt(logits, h_post, X, F, fmt="int8", iters: int = 0, out=None):
+    """proj_mix_fwd that also writes the 8-bit checkpoints of X and F.  Returns
+    (Y, H_res, Xq, Fq)."""
+    T, C = _mix_shapes(X, F)
+    f = _mx_format(fmt, _CKPT_FORMATS)
+    _need(logits, "logits", torch.float32, (T, 4, 4))
+    _need(h_post, "h_post", torch.float32, (T, 4))
+    Y = torch.empty_like(X) if out is None else _need(out, "out", torch.bfloat16, X.shape)
+    H = torch.empty_like(logits)
+    Xq, Fq = _mx_empty((T, 4, C), fmt, X.device), _mx_empty((T, C), fmt, X.device)
+    _launch(lib().mhc_proj_mix_fwd_ckpt, logits, h_post, X, F, Y, H, Xq.codes, Xq.scales, Fq.codes, Fq.scales, T, C,
+            int(iters), f)
+    return Y, H, Xq, Fq
+
+
+def _streams_shape(t, name):
+    if t.dim() != 3 or t.shape[1] != 4:
+        raise ValueError("%s must be [T, 4, C], got %s" % (name, tuple(t.shape)))
+    return int(t.shape[0]), int(t.shape[2])
+
+
+def _same_format(a, b):
+    if a.fmt != b.fmt:
+        raise ValueError("Xq and Fq must be of one format, got %s and %s" % (a.fmt, b.fmt))
+
+
+def residual_mix_bwd_ckpt(Xq: MxTensor, H_res, h_post, Fq: MxTensor, dY, need_dH=True, need_dh_post=True,
+                          need_dlogits=False):
+    """residual_mix_bwd from the checkpoints of X and F.  Returns the same dict: dX
+    and dF as from X and F themselves, dH_res, dh_post and dlogits at the
+    restored X and F."""
+    _need(dY, "dY", torch.bfloat16)
+    T, C = _streams_shape(dY, "dY")
+    _need_mx(Xq, "Xq", _CKPT_FORMATS, (T, 4, C))
+    _need_mx(Fq, "Fq", _CKPT_FORMATS, (T, C))
+    _same_format(Xq, Fq)
+    _need(H_res, "H_res", torch.float32, (T, 4, 4))
+    _need(h_post, "h_post", torch.float32, (T, 4))
+    dX = torch.empty_like(dY)
+    dF = torch.empty((T, C), dtype=torch.bfloat16, device=dY.device)
+    dH = torch.empty_like(H_res) if need_dH else None
+    dh = torch.empty_like(h_post) if need_dh_post else None
+    dl = torch.empty_like(H_res) if need_dlogits else None
+    _launch(lib().mhc_residual_mix_bwd_ckpt, Xq.codes, Xq.scales, H_res, h_post, Fq.codes, Fq.scales, dY, dX, dH, dh,
+            dF, dl, T, C, _MX_FORMATS[Xq.fmt])
+    return {"dX": dX, "dF": dF, "dH_res": dH, "dh_post": dh, "dlogits": dl}
+
+
+def proj_mix_bwd_ckpt(H_res, h_post, Xq: MxTensor, Fq: MxTensor, dY):
+    """proj_mix_bwd from the checkpoints of X and F.  Returns (dX, dlogits, dh_post, dF)."""
+    o = residual_mix_bwd_ckpt(Xq, H_res, h_post, Fq, dY, need_dH=False, need_dlogits=True)
+    return o["dX"], o["dlogits"], o["dh_post"], o["dF"]
+
+
+def mix_post_bwd_ckpt(dY, Fq: MxTensor, h_post):
+    """mix_post_bwd from the checkpoint of F: (dF, dh_post)."""
+    _need(dY, "dY", torch.bfloat16)
+    T, C = _streams_shape(dY, "dY")
+    _need_mx(Fq, "Fq", _CKPT_FORMATS, (T, C))
+    _need(h_post, "h_post", torch.float32, (T, 4))
+    dF = torch.empty((T, C), dtype=torch.bfloat16, device=dY.device)
+    dh = torch.empty_like(h_post)
+    _launch(lib().mhc_mix_post_bwd_ckpt, dY, Fq.codes, Fq.scales, h_post, dF, dh, T, C, _MX_FORMATS[Fq.fmt])
+    return dF, dh
+
+
+def mix_premap_bwd_ckpt(Xq: MxTensor, H_res, h_pre, dY, dx_in, need_dH=False, need_dlogits=True):
+    """mix_premap_bwd from the checkpoint of X.  Returns the same dict."""
+    _need(dY, "dY", torch.bfloat16)
+    T, C = _streams_shape(dY, "dY")
+    _need_mx(Xq, "Xq", _CKPT_FORMATS, (T, 4, C))
+    _need(H_res, "H_res", torch.float32, (T, 4, 4))
+    _need(h_pre, "h_pre", torch.float32, (T, 4))
+    _need(dx_in, "dx_in", torch.bfloat16, (T, C))
+    dX = torch.empty_like(dY)
+    dhp = torch.empty_like(h_pre)
+    dH = torch.empty_like(H_res) if need_dH else None
+    dl = torch.empty_like(H_res) if need_dlogits else None
+    _launch(lib().mhc_mix_premap_bwd_ckpt, Xq.codes, Xq.scales, H_res, h_pre, dY, dx_in, dX, dH, dhp, dl, T, C,
+            _MX_FORMATS[Xq.fmt])
+    return {"dX": dX, "dh_pre": dhp, "dH_res": dH, "dlogits": dl}
+
+
+def premap_fwd_mx4(X, h_pre) -> MxTensor:
+    """premap_fwd with the layer's input as "e2m1" codes [T, C], for mx4_linear
+    (quantised from the fp32 sums)."""
+    _need(X, "X", torch.bfloat16)
+    T, C = _streams_shape(X, "X")
+    _need(h_pre, "h_pre", torch.float32, (T, 4))
+    out = _mx_empty((T, C), "e2m1", X.device)
+    _launch(lib().mhc_premap_fwd_mx4, X, h_pre, out.codes, out.scales, T, C)
+    return out
+
+
+def _product_shapes(a, w):
+    sa, sw = _need_mx(a, "a", ("e2m1",)), _need_mx(w, "w", ("e2m1",))
+    if len(sa) != 2 or len(sw) != 2 or sa[1] != sw[1]:
+        raise ValueError("a and w must be [T, K] and [N, K], got %s and %s" % (sa, sw))
+    return sa[0], sw[0], sa[1]
+
+
+def mx4_linear(a: MxTensor, w: MxTensor, out=None):
+    """out[t, n] = sum_k a[t, k] w[n, k] of two "e2m1" tensors, fp32 sums rounded
+    once to bf16 (K a multiple of 32, N of 8).  Forward only: the codes carry no
+    gradient."""
+    T, N, K = _product_shapes(a, w)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=a.codes.device)
+    _need(out, "out", torch.bfloat16, (T, N))
+    _launch(lib().mhc_mx4_linear, a.codes, a.scales, w.codes, w.scales, out, T, N, K)
+    return out
+
+
+def mx4_linear_mix(a: MxTensor, w: MxTensor, X, H_res, h_post, out=None):
+    """residual_mix_fwd with F[t, c] = sum_k a[t, k] w[c, k], the product's epilogue
+    (F stays in fp32 and is not written).  Returns Y."""
+    T, C, K = _product_shapes(a, w)
+    _need(X, "X", torch.bfloat16, (T, 4, C))
+    _need(H_res, "H_res", torch.float32, (T, 4, 4))
+    _need(h_post, "h_post", torch.float32, (T, 4))
+    if out is None:
+        out = torch.empty_like(X)
+    _need(out, "out", torch.bfloat16, X.shape)
+    _launch(lib().mhc_mx4_linear_mix, a.codes, a.scales, w.codes, w.scales, X, H_res, h_post, out, T, C, K)
+    return out
+
+
 class BirkhoffProjection(torch.autograd.Function):
     """Autograd wrapper: Newton forward, implicit backward (saves P only)."""
 
@@ -506,3 +771,47 @@ class ProjectedMix(torch.autograd.Function):
         H, h, X, F = ctx.saved_tensors
         dX, dlogits, dh, dF = proj_mix_bwd(H, h, X, F, dY.contiguous())
         return dlogits, dh, dX, dF, None
+
+
+class ResidualMixCkpt(torch.autograd.Function):
+    """ResidualMix that keeps 8-bit checkpoints of X and F ("int8" or "e4m3") for
+    the backward in place of the tensors themselves: about half the saved bytes.
+    dX and dF are ResidualMix's; dH_res and dh_post are taken at the restored
+    X and F."""
+
+    @staticmethod
+    def forward(ctx, X, H_res, h_post, F, fmt="int8"):
+        X, H, h, F = X.contiguous(), H_res.contiguous(), h_post.contiguous(), F.contiguous()
+        Y, Xq, Fq = residual_mix_fwd_ckpt(X, H, h, F, fmt)
+        ctx.fmt = fmt
+        ctx.save_for_backward(H, h, Xq.codes, Xq.scales, Fq.codes, Fq.scales)
+        return Y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        H, h, xc, xs, fc, fs = ctx.saved_tensors
+        o = residual_mix_bwd_ckpt(MxTensor(xc, xs, ctx.fmt), H, h, MxTensor(fc, fs, ctx.fmt), dY.contiguous(),
+                                  need_dH=ctx.needs_input_grad[1], need_dh_post=ctx.needs_input_grad[2])
+        return o["dX"], o["dH_res"], o["dh_post"], o["dF"], None
+
+
+class ProjectedMixCkpt(torch.autograd.Function):
+    """ProjectedMix that keeps 8-bit checkpoints of X and F ("int8" or "e4m3") for
+    the backward in place of the tensors themselves."""
+
+    @staticmethod
+    def forward(ctx, logits, h_post, X, F, fmt="int8", iters: int = 0):
+        logits, h, X, F = logits.contiguous(), h_post.contiguous(), X.contiguous(), F.contiguous()
+        Y, H, Xq, Fq = proj_mix_fwd_ckpt(logits, h, X, F, fmt, iters)
+        ctx.fmt = fmt
+        ctx.save_for_backward(H, h, Xq.codes, Xq.scales, Fq.codes, Fq.scales)
+        return Y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        H, h, xc, xs, fc, fs = ctx.saved_tensors
+        dX, dlogits, dh, dF = proj_mix_bwd_ckpt(H, h, MxTensor(xc, xs, ctx.fmt), MxTensor(fc, fs, ctx.fmt),
+                                                dY.contiguous())
+        return dlogits, dh, dX, dF, None, None

@@ -55,6 +55,39 @@ cudaError_t launch_mix_post_bwd(const uint16_t* dY, const uint16_t* F, const flo
 cudaError_t launch_mix_premap_bwd(const uint16_t* X, const float* H, const float* hpre, const uint16_t* dY,
                                   const uint16_t* dx_in, uint16_t* dX, float* dH, float* dhpre, float* dlogits,
                                   int64_t T, int64_t C, cudaStream_t s);
+// Microscaled rows (mx_common.cuh); `format` is one of enum mhc_mx_format.
+cudaError_t launch_mx_pack(const uint16_t* x, uint8_t* codes, uint8_t* scales, int64_t R, int64_t C, int format,
+                           cudaStream_t s);
+cudaError_t launch_mx_unpack(const uint8_t* codes, const uint8_t* scales, uint16_t* x, int64_t R, int64_t C,
+                             int format, cudaStream_t s);
+
+// The mix with 8-bit checkpoints of X and F (mhc_ckpt.cu).
+cudaError_t launch_mix_fwd_ckpt(const uint16_t* X, const float* H, const float* hpost, const uint16_t* F, uint16_t* Y,
+                                uint8_t* Xc, uint8_t* Xs, uint8_t* Fc, uint8_t* Fs, int64_t T, int64_t C, int format,
+                                cudaStream_t s);
+cudaError_t launch_proj_mix_fwd_ckpt(const float* logits, const float* hpost, const uint16_t* X, const uint16_t* F,
+                                     uint16_t* Y, float* H, uint8_t* Xc, uint8_t* Xs, uint8_t* Fc, uint8_t* Fs,
+                                     int64_t T, int64_t C, int maxit, int format, cudaStream_t s);
+cudaError_t launch_mix_bwd_ckpt(const uint8_t* Xc, const uint8_t* Xs, const float* H, const float* hpost,
+                                const uint8_t* Fc, const uint8_t* Fs, const uint16_t* dY, uint16_t* dX, float* dH,
+                                float* dhpost, uint16_t* dF, float* dlogits, int64_t T, int64_t C, int format,
+                                cudaStream_t s);
+cudaError_t launch_mix_post_bwd_ckpt(const uint16_t* dY, const uint8_t* Fc, const uint8_t* Fs, const float* hpost,
+                                     uint16_t* dF, float* dhpost, int64_t T, int64_t C, int format, cudaStream_t s);
+cudaError_t launch_mix_premap_bwd_ckpt(const uint8_t* Xc, const uint8_t* Xs, const float* H, const float* hpre,
+                                       const uint16_t* dY, const uint16_t* dx_in, uint16_t* dX, float* dH,
+                                       float* dhpre, float* dlogits, int64_t T, int64_t C, int format,
+                                       cudaStream_t s);
+
+// The 4-bit read map, product, and product with the mix (mhc_mx4.cu).
+cudaError_t launch_premap_fwd_mx4(const uint16_t* X, const float* hpre, uint8_t* codes, uint8_t* scales, int64_t T,
+                                  int64_t C, cudaStream_t s);
+cudaError_t launch_mx4_linear(const uint8_t* A, const uint8_t* As, const uint8_t* W, const uint8_t* Ws, uint16_t* out,
+                              int64_t T, int64_t N, int64_t K, cudaStream_t s);
+cudaError_t launch_mx4_linear_mix(const uint8_t* A, const uint8_t* As, const uint8_t* W, const uint8_t* Ws,
+                                  const uint16_t* X, const float* H, const float* hpost, uint16_t* Y, int64_t T,
+                                  int64_t C, int64_t K, cudaStream_t s);
+
 cudaError_t launch_composite_gain(const float* P, float* M, float* gain_rows, float* gain_cols, int64_t L, int64_t T,
                                   cudaStream_t s);
 

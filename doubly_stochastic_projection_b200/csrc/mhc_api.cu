@@ -34,6 +34,18 @@ int check_mix_sizes(int64_t T, int64_t C)
     return MHC_OK;
 }
 
+// T rows of K 4-bit elements times N rows of K: the tensor copies address
+// rows with 32-bit coordinates.
+int check_product_sizes(int64_t T, int64_t N, int64_t K)
+{
+    if (T < 0 || T >= (int64_t(1) << 31) - 512) return MHC_ERR_SIZE;
+    if (N <= 0 || (N % 8) != 0 || N > kMaxC || K <= 0 || (K % MHC_MX_BLOCK) != 0 || K > kMaxC) return MHC_ERR_SIZE;
+    if (T > 0 && (T > kMaxElems / K || T > kMaxElems / N)) return MHC_ERR_SIZE;
+    return MHC_OK;
+}
+
+bool is_checkpoint_format(int format) { return format == MHC_MX_INT8 || format == MHC_MX_E4M3; }
+
 int resolve_iters(int method, int iters, int* out)
 {
     if (iters < 0 || iters > MHC_MAX_ITERS) return MHC_ERR_ARG;
@@ -282,6 +294,154 @@ int mhc_mix_premap_bwd(const uint16_t* X, const float* H_res, const float* h_pre
         misaligned(dX) || misaligned(dH_res) || misaligned(dh_pre) || misaligned(dlogits))
         return MHC_ERR_ALIGN;
     return cuda_status(mhc::launch_mix_premap_bwd(X, H_res, h_pre, dY, dx_in, dX, dH_res, dh_pre, dlogits, T, C,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+int mhc_mx_pack(const uint16_t* x, uint8_t* codes, uint8_t* scales, int64_t R, int64_t C, int format, void* stream)
+{
+    if (R < 0 || C <= 0 || (C % 8) != 0 || C > kMaxC || R > kMaxElems / C) return MHC_ERR_SIZE;
+    if (!is_checkpoint_format(format) && format != MHC_MX_E2M1) return MHC_ERR_ARG;
+    if (R == 0) return MHC_OK;
+    if (!x || !codes || !scales) return MHC_ERR_NULL;
+    if (misaligned(x) || misaligned(codes) || misaligned(scales)) return MHC_ERR_ALIGN;
+    return cuda_status(mhc::launch_mx_pack(x, codes, scales, R, C, format, static_cast<cudaStream_t>(stream)));
+}
+
+int mhc_mx_unpack(const uint8_t* codes, const uint8_t* scales, uint16_t* x, int64_t R, int64_t C, int format,
+                  void* stream)
+{
+    if (R < 0 || C <= 0 || (C % 8) != 0 || C > kMaxC || R > kMaxElems / C) return MHC_ERR_SIZE;
+    if (!is_checkpoint_format(format) && format != MHC_MX_E2M1) return MHC_ERR_ARG;
+    if (R == 0) return MHC_OK;
+    if (!codes || !scales || !x) return MHC_ERR_NULL;
+    if (misaligned(codes) || misaligned(scales) || misaligned(x)) return MHC_ERR_ALIGN;
+    return cuda_status(mhc::launch_mx_unpack(codes, scales, x, R, C, format, static_cast<cudaStream_t>(stream)));
+}
+
+int mhc_residual_mix_fwd_ckpt(const uint16_t* X, const float* H_res, const float* h_post, const uint16_t* F,
+                              uint16_t* Y, uint8_t* X_codes, uint8_t* X_scales, uint8_t* F_codes, uint8_t* F_scales,
+                              int64_t T, int64_t C, int format, void* stream)
+{
+    int rc = check_mix_sizes(T, C);
+    if (rc != MHC_OK) return rc;
+    if (!is_checkpoint_format(format)) return MHC_ERR_ARG;
+    if (T == 0) return MHC_OK;
+    if (!X || !H_res || !h_post || !F || !Y || !X_codes || !X_scales || !F_codes || !F_scales) return MHC_ERR_NULL;
+    if (misaligned(X) || misaligned(H_res) || misaligned(h_post) || misaligned(F) || misaligned(Y) ||
+        misaligned(X_codes) || misaligned(X_scales) || misaligned(F_codes) || misaligned(F_scales))
+        return MHC_ERR_ALIGN;
+    return cuda_status(mhc::launch_mix_fwd_ckpt(X, H_res, h_post, F, Y, X_codes, X_scales, F_codes, F_scales, T, C,
+                                                format, static_cast<cudaStream_t>(stream)));
+}
+
+int mhc_proj_mix_fwd_ckpt(const float* logits, const float* h_post, const uint16_t* X, const uint16_t* F, uint16_t* Y,
+                          float* H_res, uint8_t* X_codes, uint8_t* X_scales, uint8_t* F_codes, uint8_t* F_scales,
+                          int64_t T, int64_t C, int iters, int format, void* stream)
+{
+    int rc = check_mix_sizes(T, C);
+    if (rc != MHC_OK) return rc;
+    if (!is_checkpoint_format(format)) return MHC_ERR_ARG;
+    int it = 0;
+    if ((rc = resolve_iters(MHC_NEWTON, iters, &it)) != MHC_OK) return rc;
+    if (T == 0) return MHC_OK;
+    if (!logits || !h_post || !X || !F || !Y || !H_res || !X_codes || !X_scales || !F_codes || !F_scales)
+        return MHC_ERR_NULL;
+    if (misaligned(logits) || misaligned(h_post) || misaligned(X) || misaligned(F) || misaligned(Y) ||
+        misaligned(H_res) || misaligned(X_codes) || misaligned(X_scales) || misaligned(F_codes) ||
+        misaligned(F_scales))
+        return MHC_ERR_ALIGN;
+    return cuda_status(mhc::launch_proj_mix_fwd_ckpt(logits, h_post, X, F, Y, H_res, X_codes, X_scales, F_codes,
+                                                     F_scales, T, C, it, format, static_cast<cudaStream_t>(stream)));
+}
+
+int mhc_residual_mix_bwd_ckpt(const uint8_t* X_codes, const uint8_t* X_scales, const float* H_res,
+                              const float* h_post, const uint8_t* F_codes, const uint8_t* F_scales,
+                              const uint16_t* dY, uint16_t* dX, float* dH_res, float* dh_post, uint16_t* dF,
+                              float* dlogits, int64_t T, int64_t C, int format, void* stream)
+{
+    int rc = check_mix_sizes(T, C);
+    if (rc != MHC_OK) return rc;
+    if (!is_checkpoint_format(format)) return MHC_ERR_ARG;
+    if (T == 0) return MHC_OK;
+    if (!X_codes || !X_scales || !H_res || !h_post || !F_codes || !F_scales || !dY || !dX || !dF) return MHC_ERR_NULL;
+    if (misaligned(X_codes) || misaligned(X_scales) || misaligned(H_res) || misaligned(h_post) ||
+        misaligned(F_codes) || misaligned(F_scales) || misaligned(dY) || misaligned(dX) || misaligned(dH_res) ||
+        misaligned(dh_post) || misaligned(dF) || misaligned(dlogits))
+        return MHC_ERR_ALIGN;
+    return cuda_status(mhc::launch_mix_bwd_ckpt(X_codes, X_scales, H_res, h_post, F_codes, F_scales, dY, dX, dH_res,
+                                                dh_post, dF, dlogits, T, C, format,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+int mhc_mix_post_bwd_ckpt(const uint16_t* dY, const uint8_t* F_codes, const uint8_t* F_scales, const float* h_post,
+                          uint16_t* dF, float* dh_post, int64_t T, int64_t C, int format, void* stream)
+{
+    int rc = check_mix_sizes(T, C);
+    if (rc != MHC_OK) return rc;
+    if (!is_checkpoint_format(format)) return MHC_ERR_ARG;
+    if (T == 0) return MHC_OK;
+    if (!dY || !F_codes || !F_scales || !h_post || !dF || !dh_post) return MHC_ERR_NULL;
+    if (misaligned(dY) || misaligned(F_codes) || misaligned(F_scales) || misaligned(h_post) || misaligned(dF) ||
+        misaligned(dh_post))
+        return MHC_ERR_ALIGN;
+    return cuda_status(mhc::launch_mix_post_bwd_ckpt(dY, F_codes, F_scales, h_post, dF, dh_post, T, C, format,
+                                                     static_cast<cudaStream_t>(stream)));
+}
+
+int mhc_mix_premap_bwd_ckpt(const uint8_t* X_codes, const uint8_t* X_scales, const float* H_res, const float* h_pre,
+                            const uint16_t* dY, const uint16_t* dx_in, uint16_t* dX, float* dH_res, float* dh_pre,
+                            float* dlogits, int64_t T, int64_t C, int format, void* stream)
+{
+    int rc = check_mix_sizes(T, C);
+    if (rc != MHC_OK) return rc;
+    if (!is_checkpoint_format(format)) return MHC_ERR_ARG;
+    if (T == 0) return MHC_OK;
+    if (!X_codes || !X_scales || !H_res || !h_pre || !dY || !dx_in || !dX || !dh_pre) return MHC_ERR_NULL;
+    if (misaligned(X_codes) || misaligned(X_scales) || misaligned(H_res) || misaligned(h_pre) || misaligned(dY) ||
+        misaligned(dx_in) || misaligned(dX) || misaligned(dH_res) || misaligned(dh_pre) || misaligned(dlogits))
+        return MHC_ERR_ALIGN;
+    return cuda_status(mhc::launch_mix_premap_bwd_ckpt(X_codes, X_scales, H_res, h_pre, dY, dx_in, dX, dH_res, dh_pre,
+                                                       dlogits, T, C, format, static_cast<cudaStream_t>(stream)));
+}
+
+int mhc_premap_fwd_mx4(const uint16_t* X, const float* h_pre, uint8_t* codes, uint8_t* scales, int64_t T, int64_t C,
+                       void* stream)
+{
+    int rc = check_mix_sizes(T, C);
+    if (rc != MHC_OK) return rc;
+    if (T == 0) return MHC_OK;
+    if (!X || !h_pre || !codes || !scales) return MHC_ERR_NULL;
+    if (misaligned(X) || misaligned(h_pre) || misaligned(codes) || misaligned(scales)) return MHC_ERR_ALIGN;
+    return cuda_status(
+        mhc::launch_premap_fwd_mx4(X, h_pre, codes, scales, T, C, static_cast<cudaStream_t>(stream)));
+}
+
+int mhc_mx4_linear(const uint8_t* A_codes, const uint8_t* A_scales, const uint8_t* W_codes, const uint8_t* W_scales,
+                   uint16_t* out, int64_t T, int64_t N, int64_t K, void* stream)
+{
+    int rc = check_product_sizes(T, N, K);
+    if (rc != MHC_OK) return rc;
+    if (T == 0) return MHC_OK;
+    if (!A_codes || !A_scales || !W_codes || !W_scales || !out) return MHC_ERR_NULL;
+    if (misaligned(A_codes) || misaligned(A_scales) || misaligned(W_codes) || misaligned(W_scales) || misaligned(out))
+        return MHC_ERR_ALIGN;
+    return cuda_status(mhc::launch_mx4_linear(A_codes, A_scales, W_codes, W_scales, out, T, N, K,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+int mhc_mx4_linear_mix(const uint8_t* A_codes, const uint8_t* A_scales, const uint8_t* W_codes,
+                       const uint8_t* W_scales, const uint16_t* X, const float* H_res, const float* h_post,
+                       uint16_t* Y, int64_t T, int64_t C, int64_t K, void* stream)
+{
+    int rc = check_product_sizes(T, C, K);
+    if (rc == MHC_OK) rc = check_mix_sizes(T, C);
+    if (rc != MHC_OK) return rc;
+    if (T == 0) return MHC_OK;
+    if (!A_codes || !A_scales || !W_codes || !W_scales || !X || !H_res || !h_post || !Y) return MHC_ERR_NULL;
+    if (misaligned(A_codes) || misaligned(A_scales) || misaligned(W_codes) || misaligned(W_scales) || misaligned(X) ||
+        misaligned(H_res) || misaligned(h_post) || misaligned(Y))
+        return MHC_ERR_ALIGN;
+    return cuda_status(mhc::launch_mx4_linear_mix(A_codes, A_scales, W_codes, W_scales, X, H_res, h_post, Y, T, C, K,
                                                   static_cast<cudaStream_t>(stream)));
 }
 

@@ -1,0 +1,587 @@
+// mhc_ckpt.cu -- 8-bit checkpoints of the residual streams on sm_100a: packing
+// and restoring microscaled rows, the mix forward that writes the checkpoint
+// of X and F in the pass that reads them, and the backward kernels that read
+// the checkpoint instead of X and F.
+//
+// The mix's backward needs X and F only for dH_res and dh_post (and dh_pre).
+// Kept in bf16 they are 10 C bytes a token between forward and backward, four
+// times what a one-stream residual saves; as blocks of 32 channels with 8-bit
+// elements (mx_common.cuh) they are 5.16 C.  Y, dX and dF do not depend on the
+// checkpoint and equal those of the bf16 path; dH_res, dh_post and dh_pre are
+// the gradients at the restored streams.
+//
+// All are HBM-bound streaming kernels in the layout of mhc_mix.cu: one CTA
+// owns a token, a thread moves vectors of 8 channels, 16 bytes of bf16 or 8
+// of codes.  Four neighbouring lanes hold a block, so its largest magnitude
+// takes two shuffles.  Bytes a token: forward 10 C read, 13.16 C written;
+// backward 13.16 C read, 10 C written (28 C in bf16); split backward
+// 11.03 C + 22.13 C (38 C in bf16).
+#include "birkhoff_math.cuh"
+#include "launch.h"
+#include "mix_common.cuh"
+#include "mx_common.cuh"
+
+namespace mhc {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kFusedTok = 4;  // tokens projected together per CTA round
+
+// ------------------------------------------------------------ pack, restore
+
+// kPackThreads / lanes rows at a time: `lanes` (a power of two, 4..256) threads
+// walk one row, so that narrow rows share a CTA.
+constexpr int kPackThreads = 256;
+
+template <int kFmt>
+__device__ __forceinline__ void store_codes(uint8_t* row, int v, const uint2 w)
+{
+    if (kFmt == MHC_MX_E2M1)
+        __stcs(reinterpret_cast<uint32_t*>(row) + v, w.x);
+    else
+        __stcs(reinterpret_cast<uint2*>(row) + v, w);
+}
+
+template <int kFmt>
+__device__ __forceinline__ uint2 load_codes(const uint8_t* row, int v)
+{
+    if (kFmt == MHC_MX_E2M1) return make_uint2(__ldcs(reinterpret_cast<const uint32_t*>(row) + v), 0u);
+    return __ldcs(reinterpret_cast<const uint2*>(row) + v);
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(kPackThreads)
+mx_pack_kernel(const uint4* x, uint8_t* codes, uint8_t* scales, int64_t R, int CV, int lanes)
+{
+    const int rows = kPackThreads / lanes, lane = threadIdx.x & (lanes - 1);
+    const int64_t cp = mx_code_pitch(kFmt, (int64_t)CV * 8), sp = mx_scale_pitch((int64_t)CV * 8);
+    // the loops' bounds depend on the warp only: every lane takes part in the shuffles
+    for (int64_t r0 = (int64_t)blockIdx.x * rows; r0 < R; r0 += (int64_t)gridDim.x * rows) {
+        const int64_t r = r0 + threadIdx.x / lanes;
+        for (int v0 = 0; v0 < CV; v0 += lanes) {
+            const int v = v0 + lane;
+            const bool in = r < R && v < CV;
+            const uint4 q = in ? __ldcs(x + r * CV + v) : make_uint4(0u, 0u, 0u, 0u);
+            const int S = mx_scale_byte<kFmt>(mx_block_max(mx_amax8(q)));
+            float f[8];
+            unpack8(q, f);
+            if (in) {
+                store_codes<kFmt>(codes + r * cp, v, mx_encode8<kFmt>(f, S));
+                mx_store_scale(scales + r * sp, v, CV, S);
+            }
+        }
+    }
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(kPackThreads)
+mx_unpack_kernel(const uint8_t* codes, const uint8_t* scales, uint4* x, int64_t R, int CV, int lanes)
+{
+    const int rows = kPackThreads / lanes, lane = threadIdx.x & (lanes - 1);
+    const int64_t cp = mx_code_pitch(kFmt, (int64_t)CV * 8), sp = mx_scale_pitch((int64_t)CV * 8);
+    for (int64_t r = (int64_t)blockIdx.x * rows + threadIdx.x / lanes; r < R; r += (int64_t)gridDim.x * rows) {
+        for (int v = lane; v < CV; v += lanes) {
+            float f[8];
+            mx_decode8<kFmt>(load_codes<kFmt>(codes + r * cp, v), mx_scale_value(__ldg(scales + r * sp + (v >> 2))), f);
+            __stcs(x + r * CV + v, pack8(f));
+        }
+    }
+}
+
+// ------------------------------------------------- forward with a checkpoint
+
+struct CkptOut {
+    uint8_t *Xc, *Xs, *Fc, *Fs;
+};
+
+// Streams token t: X, F -> Y and the codes of X and F.
+template <int kFmt>
+__device__ __forceinline__ void mix_token_fwd_ckpt(const float (&h)[16], const float (&hp)[4], const uint4* X,
+                                                   const uint4* F, uint4* Y, const CkptOut& o, int64_t t, int CV)
+{
+    const int64_t C = (int64_t)CV * 8, sp = mx_scale_pitch(C);
+    const uint4* Xt = X + t * 4 * CV;
+    uint4* Yt = Y + t * 4 * CV;
+    // the bound depends on the warp only: every lane takes part in the shuffles
+    for (int v = threadIdx.x; (v & ~31) < CV; v += kThreads) {
+        const bool in = v < CV;
+        uint4 r[5], y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = in ? __ldcs(Xt + (int64_t)j * CV + v) : make_uint4(0u, 0u, 0u, 0u);
+        r[4] = in ? __ldcs(F + t * CV + v) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 x[4] = {r[0], r[1], r[2], r[3]};
+        mix_vec(h, hp, x, r[4], y);
+        int S[5];
+#pragma unroll
+        for (int j = 0; j < 5; ++j) S[j] = mx_scale_byte<kFmt>(mx_block_max(mx_amax8(r[j])));
+        if (in) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) __stcs(Yt + (int64_t)i * CV + v, y[i]);
+#pragma unroll
+            for (int j = 0; j < 5; ++j) {
+                float f[8];
+                unpack8(r[j], f);
+                const int64_t row = j < 4 ? t * 4 + j : t;
+                store_codes<kFmt>((j < 4 ? o.Xc : o.Fc) + row * C, v, mx_encode8<kFmt>(f, S[j]));
+                mx_store_scale((j < 4 ? o.Xs : o.Fs) + row * sp, v, CV, S[j]);
+            }
+        }
+    }
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(kThreads)
+mix_fwd_ckpt_kernel(const uint4* X, const float* H, const float* hpost, const uint4* F, uint4* Y, CkptOut o,
+                    int64_t T, int CV)
+{
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+        float h[16], hp[4];
+        load_maps(H, hpost, t, h, hp);
+        mix_token_fwd_ckpt<kFmt>(h, hp, X, F, Y, o, t, CV);
+    }
+}
+
+// Fused projection + mix with the checkpoint: proj_mix_fwd_kernel of
+// mhc_mix.cu with the checkpoint written in the same pass.
+template <int kFmt>
+__global__ void __launch_bounds__(kThreads)
+proj_mix_fwd_ckpt_kernel(const float* logits, const float* hpost, const uint4* X, const uint4* F, uint4* Y,
+                         float* Hout, CkptOut o, int64_t T, int CV, int maxit)
+{
+    __shared__ float sH[kFusedTok][16];
+    for (int64_t t0 = (int64_t)blockIdx.x * kFusedTok; t0 < T; t0 += (int64_t)gridDim.x * kFusedTok) {
+        if (threadIdx.x < kFusedTok && t0 + threadIdx.x < T) {
+            const int64_t t = t0 + threadIdx.x;
+            float a[16];
+            load16(logits + 16 * t, a);
+            newton_project(a, maxit);
+            store16(Hout + 16 * t, a);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sH[threadIdx.x][k] = a[k];
+        }
+        __syncthreads();
+        for (int k = 0; k < kFusedTok && t0 + k < T; ++k) {
+            float h[16], hp[4];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) h[q] = sH[k][q];
+            const float4 hq = __ldg(reinterpret_cast<const float4*>(hpost) + t0 + k);
+            hp[0] = hq.x;
+            hp[1] = hq.y;
+            hp[2] = hq.z;
+            hp[3] = hq.w;
+            mix_token_fwd_ckpt<kFmt>(h, hp, X, F, Y, o, t0 + k, CV);
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------ backward from a checkpoint
+
+// The prefetch ring of the bf16 backward (BwdRing in mix_common.cuh) with the
+// X rows as 8-byte vectors of codes and, for kZCodes, the Z row too (F's
+// codes; otherwise Z is dx_in in bf16).  Each coded row's scale travels with
+// it: the four bytes that hold it, by a copy of their own.  A slot is
+// kSlotBytes a thread, laid out row by row across the CTA.
+__device__ __forceinline__ void cp_async8(void* smem, const void* gmem)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
+                     static_cast<unsigned>(__cvta_generic_to_shared(smem))),
+                 "l"(gmem)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* smem, const void* gmem)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                     static_cast<unsigned>(__cvta_generic_to_shared(smem))),
+                 "l"(gmem)
+                 : "memory");
+}
+
+struct CkptIn {
+    const uint8_t *Xc, *Xs;  // codes [T][4][C], scales [T][4][pitch]
+    const uint8_t *Zc, *Zs;  // F's, or nullptr
+    const uint4* Z;          // dx_in, or nullptr
+};
+
+constexpr int kStages = 2;
+
+template <bool kZCodes>
+struct CkptRing {
+    static constexpr int kCoded = kZCodes ? 5 : 4;
+    static constexpr int kVec16 = kZCodes ? 4 : 5;  // dY rows, then dx_in
+    static constexpr int kSlotBytes = kVec16 * 16 + kCoded * 8 + kCoded * 4;
+    static constexpr int kSmemBytes = kStages * kSlotBytes * kThreads;
+
+    uint8_t* slots;
+    const uint4* dY;
+    CkptIn in;
+    int64_t ntok, ik, sp;
+    int CV, per_tok, iq, is, cs;
+
+    __device__ __forceinline__ uint4* vec16(int slot, int r) const
+    {
+        return reinterpret_cast<uint4*>(slots + slot * (kSlotBytes * kThreads)) + r * kThreads + threadIdx.x;
+    }
+    __device__ __forceinline__ uint2* codes(int slot, int r) const
+    {
+        return reinterpret_cast<uint2*>(slots + slot * (kSlotBytes * kThreads) + kVec16 * 16 * kThreads) +
+               r * kThreads + threadIdx.x;
+    }
+    __device__ __forceinline__ uint32_t* scale4(int slot, int r) const
+    {
+        return reinterpret_cast<uint32_t*>(slots + slot * (kSlotBytes * kThreads) +
+                                           (kVec16 * 16 + kCoded * 8) * kThreads) +
+               r * kThreads + threadIdx.x;
+    }
+
+    __device__ __forceinline__ CkptRing(void* smem, const uint4* dY_, const CkptIn& in_, int64_t T, int CV_)
+        : slots(static_cast<uint8_t*>(smem)), dY(dY_), in(in_), ik(0), sp(mx_scale_pitch((int64_t)CV_ * 8)), CV(CV_),
+          iq(0), is(0), cs(0)
+    {
+        per_tok = (int)threadIdx.x < CV ? (CV - 1 - (int)threadIdx.x) / kThreads + 1 : 0;
+        ntok = (int64_t)blockIdx.x < T ? (T - 1 - (int64_t)blockIdx.x) / gridDim.x + 1 : 0;
+#pragma unroll
+        for (int j = 0; j < kStages - 1; ++j) issue();
+    }
+
+    __device__ __forceinline__ int64_t tokens() const { return ntok; }
+    __device__ __forceinline__ int vectors() const { return per_tok; }
+
+    __device__ __forceinline__ void issue()
+    {
+        if (per_tok > 0 && ik < ntok) {
+            const int64_t t = (int64_t)blockIdx.x + ik * gridDim.x;
+            const int v = (int)threadIdx.x + iq * kThreads;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) cp_async16(vec16(is, r), dY + (t * 4 + r) * CV + v);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                cp_async8(codes(is, r), reinterpret_cast<const uint2*>(in.Xc) + (t * 4 + r) * CV + v);
+                cp_async4(scale4(is, r), in.Xs + (t * 4 + r) * sp + (v >> 4) * 4);
+            }
+            if (kZCodes) {
+                cp_async8(codes(is, kCoded - 1), reinterpret_cast<const uint2*>(in.Zc) + t * CV + v);
+                cp_async4(scale4(is, kCoded - 1), in.Zs + t * sp + (v >> 4) * 4);
+            } else {
+                cp_async16(vec16(is, kVec16 - 1), in.Z + t * CV + v);
+            }
+            if (++iq == per_tok) {
+                iq = 0;
+                ++ik;
+            }
+        }
+        cp_async_commit();  // an empty group past the end keeps the counting uniform
+        is = is + 1 == kStages ? 0 : is + 1;
+    }
+
+    // Starts the next copy, waits for the next vector in order and returns its slot.
+    __device__ __forceinline__ int next()
+    {
+        issue();
+        cp_async_wait<kStages - 1>();
+        const int slot = cs;
+        cs = cs + 1 == kStages ? 0 : cs + 1;
+        return slot;
+    }
+
+    // Row r's eight values at channel vector v.
+    template <int kFmt>
+    __device__ __forceinline__ void restore(int slot, int r, int v, float (&f)[8]) const
+    {
+        const int S = (int)((*scale4(slot, r) >> (8 * ((v >> 2) & 3))) & 255u);
+        mx_decode8<kFmt>(*codes(slot, r), mx_scale_value(S), f);
+    }
+
+    __device__ __forceinline__ void drain() { cp_async_wait<0>(); }
+};
+
+// dX, dF, dH, dh_post and the chained projection backward, X and F restored
+// from their codes in registers.
+template <int kFmt>
+__global__ void __launch_bounds__(kThreads)
+mix_bwd_ckpt_kernel(CkptIn in, const float* H, const float* hpost, const uint4* dY, uint4* dX, float* dH,
+                    float* dhpost, uint4* dF, float* dlogits, int64_t T, int CV)
+{
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float red[kWarps * 20];
+    __shared__ float tot[20];
+    const int tid = threadIdx.x;
+    CkptRing<true> ring(ring_smem, dY, in, T, CV);
+    for (int64_t k = 0; k < ring.tokens(); ++k) {
+        const int64_t t = (int64_t)blockIdx.x + k * gridDim.x;
+        if (tid == 0 && k + 1 < ring.tokens()) {
+            prefetch_l2(H + 16 * (t + gridDim.x));
+            prefetch_l2(hpost + 4 * (t + gridDim.x));
+        }
+        float h[16], hp[4];
+        load_maps(H, hpost, t, h, hp);
+        uint4* dXt = dX + t * 4 * CV;
+        uint4* dFt = dF + t * CV;
+        float acc[20];
+#pragma unroll
+        for (int q = 0; q < 20; ++q) acc[q] = 0.0f;
+        for (int q = 0; q < ring.vectors(); ++q) {
+            const int slot = ring.next();
+            const int v = tid + q * kThreads;
+            float dyf[4][8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unpack8(*ring.vec16(slot, i), dyf[i]);
+#pragma unroll
+            for (int j = 0; j < 5; ++j) {
+                float xf[8];
+                ring.template restore<kFmt>(slot, j, v, xf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float& a = acc[j < 4 ? 4 * i + j : 16 + i];
+                        a = fmaf(dyf[i][e], xf[e], a);
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 5; ++j) {
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float s = (j < 4 ? h[j] : hp[0]) * dyf[0][e];
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) s = fmaf(j < 4 ? h[4 * i + j] : hp[i], dyf[i][e], s);
+                    o[e] = s;
+                }
+                __stcs(j < 4 ? dXt + (int64_t)j * CV + v : dFt + v, pack8(o));
+            }
+        }
+        block_sum<20>(acc, red, tot);
+        if (tid < 16) {
+            if (dH) dH[16 * t + tid] = tot[tid];
+        } else if (tid < 20) {
+            if (dhpost) dhpost[4 * t + tid - 16] = tot[tid];
+        }
+        if (dlogits != nullptr && tid == 0) {
+            float g[16], out[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) g[q] = tot[q];
+            implicit_vjp(h, g, out);
+            store16(dlogits + 16 * t, out);
+        }
+        // tot is rewritten only after the next token's first barrier, which
+        // every reader above reaches after its read: no barrier needed here
+    }
+    ring.drain();
+}
+
+// Post part of the split backward: dF and dh_post from dY and F's codes.
+template <int kFmt>
+__global__ void __launch_bounds__(kThreads)
+mix_post_bwd_ckpt_kernel(const uint4* dY, const uint8_t* Fc, const uint8_t* Fs, const float* hpost, uint4* dF,
+                         float* dhpost, int64_t T, int CV)
+{
+    __shared__ float red[kWarps * 4];
+    __shared__ float tot[4];
+    const int64_t C = (int64_t)CV * 8, sp = mx_scale_pitch(C);
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(hpost) + t);
+        const float hp[4] = {q.x, q.y, q.z, q.w};
+        const uint4* dYt = dY + t * 4 * CV;
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int v = threadIdx.x; v < CV; v += kThreads) {
+            float ff[8], o[8];
+            mx_decode8<kFmt>(load_codes<kFmt>(Fc + t * C, v), mx_scale_value(__ldg(Fs + t * sp + (v >> 2))), ff);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float dyf[8];
+                unpack8(__ldcs(dYt + (int64_t)i * CV + v), dyf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    o[e] = fmaf(hp[i], dyf[e], o[e]);
+                    acc[i] = fmaf(dyf[e], ff[e], acc[i]);
+                }
+            }
+            __stcs(dF + t * CV + v, pack8(o));
+        }
+        block_sum<4>(acc, red, tot);
+        if (threadIdx.x < 4) dhpost[4 * t + threadIdx.x] = tot[threadIdx.x];
+    }
+}
+
+// Main part of the split backward with the pre-map's: dX, dH, dh_pre and the
+// chained projection backward, X restored from its codes in registers.
+template <int kFmt>
+__global__ void __launch_bounds__(kThreads)
+mix_premap_bwd_ckpt_kernel(CkptIn in, const float* H, const float* hpre, const uint4* dY, uint4* dX, float* dH,
+                           float* dhpre, float* dlogits, int64_t T, int CV)
+{
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float red[kWarps * 20];
+    __shared__ float tot[20];
+    const int tid = threadIdx.x;
+    CkptRing<false> ring(ring_smem, dY, in, T, CV);
+    for (int64_t k = 0; k < ring.tokens(); ++k) {
+        const int64_t t = (int64_t)blockIdx.x + k * gridDim.x;
+        if (tid == 0 && k + 1 < ring.tokens()) {
+            prefetch_l2(H + 16 * (t + gridDim.x));
+            prefetch_l2(hpre + 4 * (t + gridDim.x));
+        }
+        float h[16], s[4];
+        load_maps(H, hpre, t, h, s);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = sigmoidf(s[j]);
+        uint4* dXt = dX + t * 4 * CV;
+        float acc[20];
+#pragma unroll
+        for (int q = 0; q < 20; ++q) acc[q] = 0.0f;
+        for (int u = 0; u < ring.vectors(); ++u) {
+            const int slot = ring.next();
+            const int v = tid + u * kThreads;
+            float dyf[4][8], g[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unpack8(*ring.vec16(slot, i), dyf[i]);
+            unpack8(*ring.vec16(slot, 4), g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float xf[8], o[8];
+                ring.template restore<kFmt>(slot, j, v, xf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[4 * i + j] = fmaf(dyf[i][e], xf[e], acc[4 * i + j]);
+                    acc[16 + j] = fmaf(g[e], xf[e], acc[16 + j]);
+                    float a = s[j] * g[e];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a = fmaf(h[4 * i + j], dyf[i][e], a);
+                    o[e] = a;
+                }
+                __stcs(dXt + (int64_t)j * CV + v, pack8(o));
+            }
+        }
+        block_sum<20>(acc, red, tot);
+        if (tid < 16) {
+            if (dH) dH[16 * t + tid] = tot[tid];
+        } else if (tid < 20) {
+            dhpre[4 * t + tid - 16] = sigmoid_grad(hpre[4 * t + tid - 16]) * tot[tid];
+        }
+        if (dlogits != nullptr && tid == 0) {
+            float gH[16], out[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) gH[q] = tot[q];
+            implicit_vjp(h, gH, out);
+            store16(dlogits + 16 * t, out);
+        }
+        // as in mix_bwd_ckpt_kernel: the next token's first barrier orders tot
+    }
+    ring.drain();
+}
+
+// Threads that walk one row: the power of two (4..256) that covers it, so
+// that rows of a few vectors share a CTA.
+int pack_lanes(int CV)
+{
+    int lanes = 4;
+    while (lanes < CV && lanes < kPackThreads) lanes *= 2;
+    return lanes;
+}
+
+template <int kFmt>
+cudaError_t pack(const uint16_t* x, uint8_t* codes, uint8_t* scales, int64_t R, int CV, cudaStream_t s)
+{
+    const int lanes = pack_lanes(CV), rows = kPackThreads / lanes;
+    const int grid = persistent_grid((const void*)mx_pack_kernel<kFmt>, kPackThreads, 0, (R + rows - 1) / rows);
+    mx_pack_kernel<kFmt><<<grid, kPackThreads, 0, s>>>((const uint4*)x, codes, scales, R, CV, lanes);
+    return cudaGetLastError();
+}
+
+template <int kFmt>
+cudaError_t unpack(const uint8_t* codes, const uint8_t* scales, uint16_t* x, int64_t R, int CV, cudaStream_t s)
+{
+    const int lanes = pack_lanes(CV), rows = kPackThreads / lanes;
+    const int grid = persistent_grid((const void*)mx_unpack_kernel<kFmt>, kPackThreads, 0, (R + rows - 1) / rows);
+    mx_unpack_kernel<kFmt><<<grid, kPackThreads, 0, s>>>(codes, scales, (uint4*)x, R, CV, lanes);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_mx_pack(const uint16_t* x, uint8_t* codes, uint8_t* scales, int64_t R, int64_t C, int format,
+                           cudaStream_t s)
+{
+    const int CV = (int)(C / 8);
+    if (format == MHC_MX_INT8) return pack<MHC_MX_INT8>(x, codes, scales, R, CV, s);
+    if (format == MHC_MX_E4M3) return pack<MHC_MX_E4M3>(x, codes, scales, R, CV, s);
+    return pack<MHC_MX_E2M1>(x, codes, scales, R, CV, s);
+}
+
+cudaError_t launch_mx_unpack(const uint8_t* codes, const uint8_t* scales, uint16_t* x, int64_t R, int64_t C,
+                             int format, cudaStream_t s)
+{
+    const int CV = (int)(C / 8);
+    if (format == MHC_MX_INT8) return unpack<MHC_MX_INT8>(codes, scales, x, R, CV, s);
+    if (format == MHC_MX_E4M3) return unpack<MHC_MX_E4M3>(codes, scales, x, R, CV, s);
+    return unpack<MHC_MX_E2M1>(codes, scales, x, R, CV, s);
+}
+
+cudaError_t launch_mix_fwd_ckpt(const uint16_t* X, const float* H, const float* hpost, const uint16_t* F, uint16_t* Y,
+                                uint8_t* Xc, uint8_t* Xs, uint8_t* Fc, uint8_t* Fs, int64_t T, int64_t C, int format,
+                                cudaStream_t s)
+{
+    const auto kernel = format == MHC_MX_INT8 ? mix_fwd_ckpt_kernel<MHC_MX_INT8> : mix_fwd_ckpt_kernel<MHC_MX_E4M3>;
+    const int grid = persistent_grid((const void*)kernel, kThreads, 0, T);
+    kernel<<<grid, kThreads, 0, s>>>((const uint4*)X, H, hpost, (const uint4*)F, (uint4*)Y, CkptOut{Xc, Xs, Fc, Fs}, T,
+                                     (int)(C / 8));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_proj_mix_fwd_ckpt(const float* logits, const float* hpost, const uint16_t* X, const uint16_t* F,
+                                     uint16_t* Y, float* H, uint8_t* Xc, uint8_t* Xs, uint8_t* Fc, uint8_t* Fs,
+                                     int64_t T, int64_t C, int maxit, int format, cudaStream_t s)
+{
+    const auto kernel =
+        format == MHC_MX_INT8 ? proj_mix_fwd_ckpt_kernel<MHC_MX_INT8> : proj_mix_fwd_ckpt_kernel<MHC_MX_E4M3>;
+    const int grid = persistent_grid((const void*)kernel, kThreads, 0, (T + kFusedTok - 1) / kFusedTok);
+    kernel<<<grid, kThreads, 0, s>>>(logits, hpost, (const uint4*)X, (const uint4*)F, (uint4*)Y, H,
+                                     CkptOut{Xc, Xs, Fc, Fs}, T, (int)(C / 8), maxit);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mix_bwd_ckpt(const uint8_t* Xc, const uint8_t* Xs, const float* H, const float* hpost,
+                                const uint8_t* Fc, const uint8_t* Fs, const uint16_t* dY, uint16_t* dX, float* dH,
+                                float* dhpost, uint16_t* dF, float* dlogits, int64_t T, int64_t C, int format,
+                                cudaStream_t s)
+{
+    const auto kernel = format == MHC_MX_INT8 ? mix_bwd_ckpt_kernel<MHC_MX_INT8> : mix_bwd_ckpt_kernel<MHC_MX_E4M3>;
+    constexpr int smem = CkptRing<true>::kSmemBytes;
+    static_assert(smem + kWarps * 20 * 4 + 80 <= 48 * 1024, "ring needs an opt-in");
+    const int grid = persistent_grid((const void*)kernel, kThreads, smem, T);
+    kernel<<<grid, kThreads, smem, s>>>(CkptIn{Xc, Xs, Fc, Fs, nullptr}, H, hpost, (const uint4*)dY, (uint4*)dX, dH,
+                                        dhpost, (uint4*)dF, dlogits, T, (int)(C / 8));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mix_post_bwd_ckpt(const uint16_t* dY, const uint8_t* Fc, const uint8_t* Fs, const float* hpost,
+                                     uint16_t* dF, float* dhpost, int64_t T, int64_t C, int format, cudaStream_t s)
+{
+    const auto kernel =
+        format == MHC_MX_INT8 ? mix_post_bwd_ckpt_kernel<MHC_MX_INT8> : mix_post_bwd_ckpt_kernel<MHC_MX_E4M3>;
+    const int grid = persistent_grid((const void*)kernel, kThreads, 0, T);
+    kernel<<<grid, kThreads, 0, s>>>((const uint4*)dY, Fc, Fs, hpost, (uint4*)dF, dhpost, T, (int)(C / 8));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mix_premap_bwd_ckpt(const uint8_t* Xc, const uint8_t* Xs, const float* H, const float* hpre,
+                                       const uint16_t* dY, const uint16_t* dx_in, uint16_t* dX, float* dH,
+                                       float* dhpre, float* dlogits, int64_t T, int64_t C, int format, cudaStream_t s)
+{
+    const auto kernel =
+        format == MHC_MX_INT8 ? mix_premap_bwd_ckpt_kernel<MHC_MX_INT8> : mix_premap_bwd_ckpt_kernel<MHC_MX_E4M3>;
+    constexpr int smem = CkptRing<false>::kSmemBytes;
+    static_assert(smem + kWarps * 20 * 4 + 80 <= 48 * 1024, "ring needs an opt-in");
+    const int grid = persistent_grid((const void*)kernel, kThreads, smem, T);
+    kernel<<<grid, kThreads, smem, s>>>(CkptIn{Xc, Xs, nullptr, nullptr, (const uint4*)dx_in}, H, hpre,
+                                        (const uint4*)dY, (uint4*)dX, dH, dhpre, dlogits, T, (int)(C / 8));
+    return cudaGetLastError();
+}
+
+}  // namespace mhc

@@ -28,28 +28,6 @@ constexpr int kMixThreads = 128;
 constexpr int kMixWarps = kMixThreads / 32;
 constexpr int kFusedTok = 4;  // tokens projected together per CTA round
 
-// One 8-channel vector of one token: y_i = sum_j h_ij x_j + hp_i f.
-__device__ __forceinline__ void mix_vec(const float (&h)[16], const float (&hp)[4], const uint4 (&x)[4],
-                                        const uint4 f, uint4 (&y)[4])
-{
-    float xf[4][8], ff[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) unpack8(x[j], xf[j]);
-    unpack8(f, ff);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float s = hp[i] * ff[e];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s = fmaf(h[4 * i + j], xf[j][e], s);
-            o[e] = s;
-        }
-        y[i] = pack8(o);
-    }
-}
-
 // Streams token t: X, F -> Y.
 __device__ __forceinline__ void mix_token_fwd(const float (&h)[16], const float (&hp)[4], const uint4* Xt,
                                               const uint4* Ft, uint4* Yt, int CV)
@@ -127,49 +105,6 @@ proj_mix_fwd_kernel(const float* logits, const float* hpost, const uint4* X, con
         }
         __syncthreads();
     }
-}
-
-// One 8-channel vector of the backward: dX, dF out; dH, dh_post partial sums.
-__device__ __forceinline__ void mix_vec_bwd(const float (&h)[16], const float (&hp)[4], const uint4 (&dy)[4],
-                                            const uint4 (&x)[4], const uint4 f, float (&acc)[20],
-                                            uint4 (&dx)[4], uint4& df)
-{
-    float dyf[4][8], xf[4][8], ff[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) unpack8(dy[i], dyf[i]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) unpack8(x[j], xf[j]);
-    unpack8(f, ff);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[4 * i + j] = fmaf(dyf[i][e], xf[j][e], acc[4 * i + j]);
-            acc[16 + i] = fmaf(dyf[i][e], ff[e], acc[16 + i]);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float s = h[j] * dyf[0][e];
-#pragma unroll
-            for (int i = 1; i < 4; ++i) s = fmaf(h[4 * i + j], dyf[i][e], s);
-            o[e] = s;
-        }
-        dx[j] = pack8(o);
-    }
-    float o[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float s = hp[0] * dyf[0][e];
-#pragma unroll
-        for (int i = 1; i < 4; ++i) s = fmaf(hp[i], dyf[i][e], s);
-        o[e] = s;
-    }
-    df = pack8(o);
 }
 
 // Backward.  Each thread streams its own 8-channel vectors (v = tid, tid + 128,

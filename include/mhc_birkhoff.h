@@ -345,6 +345,134 @@ MHC_API int mhc_mix_premap_bwd(const uint16_t *X, const float *H_res, const floa
                                float *dlogits, int64_t T, int64_t C, void *stream);
 
 /*
+ * Microscaled storage
+ * -------------------
+ * A row of C channels is stored as codes plus one scale byte for each block of
+ * 32 channels (the last block may hold fewer): value = element * 2^(S - 127).
+ * S is the smallest exponent at which the block's largest magnitude does not
+ * pass the format's largest value; elements are rounded to nearest, ties to
+ * even.  These are the block size, scale type and element types of the OCP
+ * Microscaling formats.  The pages name none; this is the library's own
+ * storage for what they say is kept or moved at high cost: the n-wide streams
+ * ([NA] on memory and recompute, [FP] "HC").
+ *
+ *   MHC_MX_INT8  m / 64, |m| <= 127     one byte a code
+ *   MHC_MX_E4M3  4 exponent, 3 mantissa bits, up to 448   one byte a code
+ *   MHC_MX_E2M1  2 exponent, 1 mantissa bit, up to 6      two codes a byte, the
+ *                even channel in the low half
+ *
+ *   codes   [R][C] uint8 (8-bit formats) or [R][C / 2] uint8 (MHC_MX_E2M1).
+ *   scales  [R][MHC_MX_SCALE_PITCH(C)] uint8: the blocks' scales in order, then
+ *           zero bytes up to a multiple of four.
+ *   A block that holds an infinity or NaN has S = 255 and codes 0, and
+ *   restores as NaN in every channel; other blocks of the row are not
+ *   affected.  A block of zeros has S = 0.  One int8 case saturates: a block
+ *   whose largest magnitude is the largest bf16 (S would be 255) keeps S = 254.
+ */
+enum mhc_mx_format {
+    MHC_MX_INT8 = 0,
+    MHC_MX_E4M3 = 1,
+    MHC_MX_E2M1 = 2
+};
+#define MHC_MX_BLOCK 32
+#define MHC_MX_SCALE_PITCH(C) (4 * (((int64_t)(C) + 127) / 128))
+
+/*
+ * mhc_mx_pack / mhc_mx_unpack -- rows of bf16 to microscaled codes and back.
+ * Restored values are exact in bf16, except that an e4m3 or e2m1 element next
+ * to 2^128 may round up to it and restore as infinity.
+ *
+ *   x [R][C] bf16, read (pack) or written (unpack); streams [T][4][C] are
+ *   R = 4 T rows.  R >= 0; C > 0, C % 8 == 0.
+ *   format  one of enum mhc_mx_format (MHC_ERR_ARG otherwise).
+ */
+MHC_API int mhc_mx_pack(const uint16_t *x, uint8_t *codes, uint8_t *scales, int64_t R, int64_t C, int format,
+                        void *stream);
+MHC_API int mhc_mx_unpack(const uint8_t *codes, const uint8_t *scales, uint16_t *x, int64_t R, int64_t C,
+                          int format, void *stream);
+
+/*
+ * mhc_residual_mix_fwd_ckpt / mhc_proj_mix_fwd_ckpt -- mhc_residual_mix_fwd and
+ * mhc_proj_mix_fwd that also write 8-bit checkpoints of X and F, in the pass
+ * that reads them: what mhc_mx_pack(X) and mhc_mx_pack(F) give.  The backward
+ * needs X and F only for dH_res, dh_post and dh_pre; kept this way between
+ * forward and backward they take 5.16 C bytes a token in place of 10 C.  Y is
+ * computed from X and F themselves, not from the codes.
+ *
+ *   X_codes [T][4][C], X_scales [T][4][MHC_MX_SCALE_PITCH(C)],
+ *   F_codes [T][C],    F_scales [T][MHC_MX_SCALE_PITCH(C)]   uint8, written.
+ *   format  MHC_MX_INT8 or MHC_MX_E4M3 (MHC_ERR_ARG otherwise).
+ *   Other arguments as in the entry points without the checkpoint.
+ */
+MHC_API int mhc_residual_mix_fwd_ckpt(const uint16_t *X, const float *H_res, const float *h_post,
+                                      const uint16_t *F, uint16_t *Y, uint8_t *X_codes, uint8_t *X_scales,
+                                      uint8_t *F_codes, uint8_t *F_scales, int64_t T, int64_t C, int format,
+                                      void *stream);
+MHC_API int mhc_proj_mix_fwd_ckpt(const float *logits, const float *h_post, const uint16_t *X, const uint16_t *F,
+                                  uint16_t *Y, float *H_res, uint8_t *X_codes, uint8_t *X_scales,
+                                  uint8_t *F_codes, uint8_t *F_scales, int64_t T, int64_t C, int iters, int format,
+                                  void *stream);
+
+/*
+ * mhc_residual_mix_bwd_ckpt, mhc_mix_post_bwd_ckpt, mhc_mix_premap_bwd_ckpt --
+ * mhc_residual_mix_bwd, mhc_mix_post_bwd and mhc_mix_premap_bwd with X and F
+ * given as checkpoints and restored in registers.  dX and dF are those of
+ * the bf16 entry points; dH_res, dh_post, dh_pre and dlogits are the gradients
+ * at the restored X and F.  mhc_proj_mix_bwd has its form here too:
+ * mhc_residual_mix_bwd_ckpt with dH_res = NULL and dlogits given.
+ *
+ *   format  that of the forward, MHC_MX_INT8 or MHC_MX_E4M3.
+ *   Other arguments as in the bf16 entry points (those optional there are
+ *   optional here).
+ */
+MHC_API int mhc_residual_mix_bwd_ckpt(const uint8_t *X_codes, const uint8_t *X_scales, const float *H_res,
+                                      const float *h_post, const uint8_t *F_codes, const uint8_t *F_scales,
+                                      const uint16_t *dY, uint16_t *dX, float *dH_res, float *dh_post,
+                                      uint16_t *dF, float *dlogits, int64_t T, int64_t C, int format,
+                                      void *stream);
+MHC_API int mhc_mix_post_bwd_ckpt(const uint16_t *dY, const uint8_t *F_codes, const uint8_t *F_scales,
+                                  const float *h_post, uint16_t *dF, float *dh_post, int64_t T, int64_t C,
+                                  int format, void *stream);
+MHC_API int mhc_mix_premap_bwd_ckpt(const uint8_t *X_codes, const uint8_t *X_scales, const float *H_res,
+                                    const float *h_pre, const uint16_t *dY, const uint16_t *dx_in, uint16_t *dX,
+                                    float *dH_res, float *dh_pre, float *dlogits, int64_t T, int64_t C, int format,
+                                    void *stream);
+
+/*
+ * mhc_premap_fwd_mx4 -- mhc_premap_fwd with the layer's input written as
+ * MHC_MX_E2M1 codes, ready for mhc_mx4_linear.  The codes are those of the
+ * fp32 sums (x_in is not rounded to bf16 first).
+ *
+ *   codes [T][C / 2], scales [T][MHC_MX_SCALE_PITCH(C)] uint8, written.
+ */
+MHC_API int mhc_premap_fwd_mx4(const uint16_t *X, const float *h_pre, uint8_t *codes, uint8_t *scales, int64_t T,
+                               int64_t C, void *stream);
+
+/*
+ * mhc_mx4_linear -- the product of two MHC_MX_E2M1 matrices,
+ *     out[t,n] = sum_k a[t,k] w[n,k]
+ * on the tensor cores, accumulated in fp32 and rounded once to bf16: the
+ * layer's first linear behind the read map, or any other.  Forward only.
+ *
+ *   A_codes [T][K / 2], A_scales [T][MHC_MX_SCALE_PITCH(K)]: the activations.
+ *   W_codes [N][K / 2], W_scales [N][MHC_MX_SCALE_PITCH(K)]: the weights.
+ *   out [T][N] bf16, written.
+ *   0 <= T < 2^31 - 512; N > 0, N % 8 == 0; K > 0, K % 32 == 0.
+ *
+ * mhc_mx4_linear_mix -- the same product as the layer output F of the residual
+ * mix, which is its epilogue: F[t,c] = sum_k a[t,k] w[c,k] stays in fp32 and
+ * is not written, and
+ *     Y[t,i,c] = sum_j H_res[t,i,j] X[t,j,c] + h_post[t,i] F[t,c]
+ *   X, Y [T][4][C] bf16, H_res [T][4][4], h_post [T][4] float; C is the
+ *   product's N.  Y must not overlap X.
+ */
+MHC_API int mhc_mx4_linear(const uint8_t *A_codes, const uint8_t *A_scales, const uint8_t *W_codes,
+                           const uint8_t *W_scales, uint16_t *out, int64_t T, int64_t N, int64_t K, void *stream);
+MHC_API int mhc_mx4_linear_mix(const uint8_t *A_codes, const uint8_t *A_scales, const uint8_t *W_codes,
+                               const uint8_t *W_scales, const uint16_t *X, const float *H_res,
+                               const float *h_post, uint16_t *Y, int64_t T, int64_t C, int64_t K, void *stream);
+
+/*
  * mhc_composite_gain -- diagnostic of the composite mixing map across depth:
  * per token, M = P_{L-1} ... P_1 P_0 (layer 0 applied first) and its largest
  * absolute row sum (forward signal gain) and column sum (gradient gain).
