@@ -77,6 +77,7 @@ def lib() -> ctypes.CDLL:
                 "mhc_mix_post_bwd_ckpt": [p] * 6 + [i64, i64, i32, p],
                 "mhc_mix_premap_bwd_ckpt": [p] * 10 + [i64, i64, i32, p],
                 "mhc_premap_fwd_mx4": [p, p, p, p, i64, i64, p],
+                "mhc_wait_status": [],
                 "mhc_mx4_linear": [p, p, p, p, p, i64, i64, i64, p],
                 "mhc_mx4_linear_mix": [p, p, p, p, p, p, p, p, i64, i64, i64, p],
                 "mhc_residual_mix_fwd": [p, p, p, p, p, i64, i64, p],
@@ -716,6 +717,12 @@ def mx4_linear_mix(a: MxTensor, w: MxTensor, X, H_res, h_post, out=None):
     _need(out, "out", torch.bfloat16, X.shape)
     _launch(lib().mhc_mx4_linear_mix, a.codes, a.scales, w.codes, w.scales, X, H_res, h_post, out, T, C, K)
     return out
+
+
+def wait_status() -> None:
+    """Raises MhcError if a bounded wait of the 4-bit products has run out on the
+    current device since the last call (mhc_wait_status); synchronises the device."""
+    _check(lib().mhc_wait_status())
 
 
 class BirkhoffProjection(torch.autograd.Function):

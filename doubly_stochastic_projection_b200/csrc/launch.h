@@ -88,6 +88,10 @@ cudaError_t launch_mx4_linear_mix(const uint8_t* A, const uint8_t* As, const uin
                                   const uint16_t* X, const float* H, const float* hpost, uint16_t* Y, int64_t T,
                                   int64_t C, int64_t K, cudaStream_t s);
 
+// Whether a bounded wait of the 4-bit products has run out since the last
+// call; synchronises the device.
+cudaError_t read_wait_status(bool* expired);
+
 cudaError_t launch_composite_gain(const float* P, float* M, float* gain_rows, float* gain_cols, int64_t L, int64_t T,
                                   cudaStream_t s);
 

@@ -445,6 +445,13 @@ int mhc_mx4_linear_mix(const uint8_t* A_codes, const uint8_t* A_scales, const ui
                                                   static_cast<cudaStream_t>(stream)));
 }
 
+int mhc_wait_status(void)
+{
+    bool expired = false;
+    const cudaError_t e = mhc::read_wait_status(&expired);
+    return e != cudaSuccess || expired ? MHC_ERR_CUDA : MHC_OK;
+}
+
 int mhc_composite_gain(const float* P_layers, float* M, float* gain_rows, float* gain_cols, int64_t L, int64_t T,
                        void* stream)
 {

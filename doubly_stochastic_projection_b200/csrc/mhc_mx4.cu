@@ -6,10 +6,17 @@
 //   read map       a[t] = codes of x_in[t,c] = sum_j sigmoid(h_pre[t,j]) X[t,j,c]
 //   product        out[t,n] = sum_b sa[t,b] sw[n,b] sum_{k in b} a[t,k] w[n,k]
 //   product + mix  Y[t,i,c] = sum_j H[t,i,j] X[t,j,c] + h_post[t,i] out[t,c]
+#include <cuda.h>
+
+#include <atomic>
+#include <climits>
+
 #include "birkhoff_math.cuh"
 #include "launch.h"
 #include "mix_common.cuh"
 #include "mx_common.cuh"
+#include "pdl.cuh"
+#include "tc5.cuh"
 
 namespace mhc {
 
@@ -52,74 +59,378 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 }
 
 // ------------------------------------------------------------------- product
+//
+// D[n, t] = W A^T on the tensor cores' block-scaled 4-bit kind: a CTA takes a
+// tile of 128 channels (the rows of tensor memory) by kTok tokens (its
+// columns) and walks K in tiles of 256 elements, 128 bytes a row.  Its warps:
+//   0     loads the code tiles by TMA (128-byte swizzle) into a ring of stages
+//   1     issues the tcgen05 instructions: scales into tensor memory, four
+//         steps of 64 a tile
+//   2, 3  bring the scales of W and A.  They are rows of bytes in memory and
+//         have to be, for the tensor cores, chunks of 512 bytes with the four
+//         bytes of rows r, r + 32, r + 64, r + 96 side by side: a lane reads 16
+//         bytes (two tiles' worth) of four rows and stores four 16-byte vectors
+//   4-11  the epilogue: tensor memory -> shared memory, turned so that a
+//         thread holds eight consecutive channels of a token -> the output
+// Two forms.  Whole: one persistent CTA an SM walks output tiles, the sums of
+// one tile in one half of tensor memory while the epilogue drains the other.
+// Split: a cluster shares one output tile, each CTA a part of K; the partial
+// sums meet in shared memory and are added in the order of the ranks.
+//
+// Every wait is bounded (tc5.cuh).  One that runs out, which no valid call
+// does, sets mx4_wait_expired, makes the other roles give up too, and leaves
+// NaN in the outputs that are not done.
 
-constexpr int kDotThreads = 256;  // one warp for each of 8 channels
-constexpr int kDotTokens = 8;
+constexpr int kChan = 128;      // channels of a tile
+constexpr int kStepBytes = 128; // bytes of K of a tile: 256 elements
+constexpr int kProdThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kEpiThreads = 32 * kEpiWarps;
 
-struct MixArgs {
-    const uint4* X;  // nullptr: the plain product
+constexpr uint64_t kDrainNs = 100000000;  // for what is in flight, once a wait has run out
+
+__device__ int mx4_wait_expired;
+
+struct ProductArgs {
+    const uint8_t *As, *Ws;
+    uint4* out;      // [T][N] bf16, or Y [T][4][N]
+    const uint4* X;  // the mix's: [T][4][N] bf16, [T][4][4], [T][4]
     const float *H, *hpost;
+    int64_t T;
+    int N, K;
+    int chan_tiles, tok_tiles;
 };
 
-// Eight tokens by eight channels a CTA: a warp holds one channel, its lanes
-// walk the blocks of 32 along K.
-template <bool kMix>
-__global__ void __launch_bounds__(kDotThreads)
-mx4_dot_kernel(const uint8_t* A, const uint8_t* As, const uint8_t* W, const uint8_t* Ws, MixArgs m, uint4* out,
-               int64_t T, int N, int K)
+template <int kTok_, int kStages_, bool kSplit_>
+struct ProductShape {
+    static constexpr int kTok = kTok_, kStages = kStages_;
+    static constexpr bool kSplit = kSplit_;
+    static constexpr int kTokChunks = (kTok + 127) / 128;  // 128-row chunks of A's scales
+    static constexpr int kWBytes = kChan * kStepBytes, kABytes = kTok * kStepBytes;
+    static constexpr int kWsBytes = 2 * 512, kAsBytes = 2 * kTokChunks * 512;
+    static constexpr int kStageBytes = kWBytes + kABytes + kWsBytes + kAsBytes;
+    static constexpr int kSums = kSplit ? 1 : 2;  // accumulator tiles
+    // the epilogue's: two buffers of 32 tokens, or the whole tile's partial sums
+    static constexpr int kEpiBytes = (kSplit ? kTok : 64) * kChan * 4;
+    static constexpr int kBars = 2 * kStages + 2 * kSums + 1;
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + 8 * kBars + 16;
+    // columns of tensor memory: sums, then each stage's scales of W and A
+    static constexpr int kScaleCols = 8 + 8 * kTokChunks;
+    static constexpr int kSumCols = (kSums * kTok + 31) / 32 * 32;
+    static constexpr int kColumns = 512;
+    static_assert(kSumCols + kStages * kScaleCols <= kColumns, "tensor memory");
+    static_assert(kABytes % 1024 == 0 && kStageBytes % 1024 == 0, "the swizzle repeats every 1024 bytes");
+    // one CTA an SM: two that hold tensor memory and wait for cluster mates
+    // could otherwise wait for each other
+    static_assert(kSmemBytes > 116 * 1024 && kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+// Four words of scales (two K tiles) of one row from word w0 on; words and
+// bytes past the row's blocks are zero.  wide: rows start on 16 bytes.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int w0, int KB, bool wide)
 {
-    __shared__ float f[kDotTokens][8];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, KB = K / kMxBlock;
-    const int64_t t0 = (int64_t)blockIdx.y * kDotTokens, sp = mx_scale_pitch(K);
-    const int n = blockIdx.x * 8 + warp;
-    float acc[kDotTokens] = {};
-    for (int b = lane; b < KB; b += 32) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(W + ((int64_t)n * K + b * kMxBlock) / 2);
-        const float sw = mx_scale_value(Ws[n * sp + b]);
-        float wf[4][8];
+    uint32_t w[4];
+    if (wide) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + 4 * w0));
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mx_decode8<MHC_MX_E2M1>(make_uint2(w[q], 0u), 1.0f, wf[q]);
-        for (int k = 0; k < kDotTokens && t0 + k < T; ++k) {
-            const uint32_t* a = reinterpret_cast<const uint32_t*>(A + ((t0 + k) * K + b * kMxBlock) / 2);
-            float s = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float af[8];
-                mx_decode8<MHC_MX_E2M1>(make_uint2(a[q], 0u), 1.0f, af);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s = fmaf(af[e], wf[q][e], s);
-            }
-            acc[k] = fmaf(s * sw, mx_scale_value(As[(t0 + k) * sp + b]), acc[k]);
-        }
+        for (int j = 0; j < 4; ++j)
+            w[j] = 4 * (w0 + j) < KB ? __ldg(reinterpret_cast<const uint32_t*>(row) + w0 + j) : 0u;
     }
 #pragma unroll
-    for (int k = 0; k < kDotTokens; ++k) {
-        const float s = warp_sum(acc[k]);
-        if (lane == 0) f[k][warp] = s;
+    for (int j = 0; j < 4; ++j) {
+        const int left = KB - 4 * (w0 + j);  // blocks that the word still holds
+        if (left < 4) w[j] = left <= 0 ? 0u : w[j] & (0xffffffffu >> (8 * (4 - left)));
     }
-    __syncthreads();
-    const int k = threadIdx.x;
-    if (k >= kDotTokens || t0 + k >= T) return;
-    const int64_t t = t0 + k;
-    const int NV = N / 8;
-    if (kMix) {
-        float h[16], hp[4];
-        load_maps(m.H, m.hpost, t, h, hp);
-        float xf[4][8];
-        for (int j = 0; j < 4; ++j) unpack8(m.X[(t * 4 + j) * NV + blockIdx.x], xf[j]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight channels of a token: vector v of N / 8.
+template <bool kMix>
+__device__ __forceinline__ void emit(const ProductArgs& p, const float (&f)[8], int64_t t, int v)
+{
+    const int NV = p.N >> 3;
+    if constexpr (kMix) {
+        uint4 x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __ldcs(p.X + (t * 4 + j) * NV + v);
+        float h[16], hp[4], xf[4][8];
+        load_maps(p.H, p.hpost, t, h, hp);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) unpack8(x[j], xf[j]);
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
             float o[8];
+#pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float s = hp[i] * f[k][e];
+                float s = hp[i] * f[e];
+#pragma unroll
                 for (int j = 0; j < 4; ++j) s = fmaf(h[4 * i + j], xf[j][e], s);
                 o[e] = s;
             }
-            out[(t * 4 + i) * NV + blockIdx.x] = pack8(o);
+            __stcs(p.out + (t * 4 + i) * NV + v, pack8(o));
         }
     } else {
-        float o[8];
-        for (int e = 0; e < 8; ++e) o[e] = f[k][e];
-        out[t * NV + blockIdx.x] = pack8(o);
+        p.out[t * NV + v] = pack8(f);
+    }
+}
+
+template <class S, bool kMix>
+__global__ void __launch_bounds__(kProdThreads, 1)
+mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapA,
+                   const ProductArgs p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    constexpr int kTok = S::kTok, kStages = S::kStages;
+    const uint32_t base = (tc5::smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - tc5::smem_addr(smem_raw));
+    float* epi = reinterpret_cast<float*>(smem + kStages * S::kStageBytes);
+    const uint32_t bars = base + kStages * S::kStageBytes + S::kEpiBytes;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kStages * S::kStageBytes + S::kEpiBytes + 8 * S::kBars);
+    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const auto full = [&](int s) { return bars + 8 * s; };
+    const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+    const auto sum_full = [&](int a) { return bars + 8 * (2 * kStages + a); };
+    const auto sum_empty = [&](int a) { return bars + 8 * (2 * kStages + S::kSums + a); };
+    const uint32_t drained = bars + 8 * (2 * kStages + 2 * S::kSums);  // used when a wait has run out
+    // offsets within a stage: W, A, scales of W, scales of A
+    constexpr int kOffA = S::kWBytes, kOffWs = kOffA + S::kABytes, kOffAs = kOffWs + S::kWsBytes;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0 && lane == 0) {
+        tc5::prefetch_map(&mapW);
+        tc5::prefetch_map(&mapA);
+        for (int s = 0; s < kStages; ++s) {
+            tc5::mbar_init(full(s), 3);  // the TMA thread and two scale warps
+            tc5::mbar_init(empty(s), 1);
+        }
+        for (int a = 0; a < S::kSums; ++a) {
+            tc5::mbar_init(sum_full(a), 1);
+            tc5::mbar_init(sum_empty(a), kEpiWarps);
+        }
+        tc5::mbar_init(drained, 1);
+        *abort = 0;
+        tc5::fence_mbar_init();
+    }
+    if (warp == 1) tc5::tmem_alloc<S::kColumns>(tc5::smem_addr(tmem_slot));
+    tc5::fence_before_sync();
+    __syncthreads();
+    tc5::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+
+    // this CTA's output tiles, and its share of K in pairs of tiles
+    const int ranks = S::kSplit ? (int)tc5::cluster_size() : 1, rank = S::kSplit ? (int)tc5::cluster_rank() : 0;
+    const int ktiles = (p.K / 2 + kStepBytes - 1) / kStepBytes, pairs = (ktiles + 1) / 2;
+    const int pair0 = pairs * rank / ranks, pair1 = pairs * (rank + 1) / ranks;
+    const int k0 = 2 * pair0, k1 = min(2 * pair1, ktiles);
+    const int tiles = p.chan_tiles * p.tok_tiles;
+    const int first = blockIdx.x / ranks, stride = gridDim.x / ranks;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int tile = first; tile < tiles && ok; tile += stride) {
+                const int n0 = tile % p.chan_tiles * kChan, t0 = tile / p.chan_tiles * kTok;
+                for (int k = k0; k < k1; ++k, ++it) {
+                    const int s = it % kStages;
+                    if (!(ok = tc5::mbar_wait(empty(s), (it / kStages & 1) ^ 1, abort))) break;
+                    const uint32_t at = base + s * S::kStageBytes;
+                    tc5::mbar_expect_tx(full(s), S::kWBytes + S::kABytes);
+                    tc5::tma_load_2d(at, &mapW, k * kStepBytes, n0, full(s));
+                    tc5::tma_load_2d(at + kOffA, &mapA, k * kStepBytes, t0, full(s));
+                }
+            }
+            if (!ok) {
+                // the copies in flight: the last kStages ones at most
+                *abort = 1;
+                for (int j = max(0, it - kStages); j < it; ++j)
+                    tc5::mbar_wait(full(j % kStages), j / kStages & 1, nullptr, kDrainNs);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t inst = tc5::mx4_instruction(kChan, kTok);
+            int it = 0, n = 0;
+            for (int tile = first; tile < tiles && ok; tile += stride, ++n) {
+                const int a = n % S::kSums;
+                if (!(ok = tc5::mbar_wait(sum_empty(a), (n / S::kSums & 1) ^ 1, abort))) break;
+                tc5::fence_after_sync();
+                const uint32_t d = tmem + a * kTok;
+                for (int k = k0; k < k1; ++k, ++it) {
+                    const int s = it % kStages;
+                    if (!(ok = tc5::mbar_wait(full(s), it / kStages & 1, abort))) break;
+                    tc5::fence_after_sync();
+                    const uint32_t at = base + s * S::kStageBytes;
+                    const uint32_t sw = tmem + S::kSumCols + s * S::kScaleCols, sa = sw + 8;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tc5::copy_scales(sw + 4 * h, tc5::scale_desc(at + kOffWs + 512 * h));
+#pragma unroll
+                        for (int c = 0; c < S::kTokChunks; ++c)
+                            tc5::copy_scales(sa + 4 * (h * S::kTokChunks + c),
+                                             tc5::scale_desc(at + kOffAs + 512 * (h * S::kTokChunks + c)));
+                    }
+                    const uint64_t dw = tc5::operand_desc(at), da = tc5::operand_desc(at + kOffA);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)  // 64 elements: 32 bytes along the swizzled row
+                        tc5::mma_mx4(d, dw + 2 * q, da + 2 * q, inst | tc5::scale_select(2 * (q & 1)), sw + 4 * (q >> 1),
+                                     sa + 4 * S::kTokChunks * (q >> 1), k > k0 || q > 0);
+                    tc5::commit(empty(s));
+                }
+                if (ok) tc5::commit(sum_full(a));
+            }
+            if (!ok) {
+                *abort = 1;  // the tensor work in flight, before its memory is freed
+                tc5::commit(drained);
+                tc5::mbar_wait(drained, 0, nullptr, kDrainNs);
+            }
+        }
+    } else if (warp < 4) {
+        // warp 2: W's rows, warp 3: A's; lane l holds rows l, l + 32, ... of the tile
+        const bool isW = warp == 2;
+        const uint8_t* src = isW ? p.Ws : p.As;
+        const int KB = p.K / kMxBlock, pitch = (int)mx_scale_pitch(p.K);
+        const bool wide = (pitch & 15) == 0;
+        const int64_t rows = isW ? (int64_t)p.N : p.T;
+        constexpr int kGroups = (kTok + 31) / 32 > 4 ? (kTok + 31) / 32 : 4;
+        const int groups = isW ? 4 : (kTok + 31) / 32;
+        uint4 cur[kGroups], nxt[kGroups];
+        const auto fetch = [&](int tile, int pair, uint4(&q)[kGroups]) {
+            const int64_t r0 = isW ? (int64_t)(tile % p.chan_tiles) * kChan : (int64_t)(tile / p.chan_tiles) * kTok;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const int64_t r = r0 + 32 * g + lane;
+                q[g] = make_uint4(0u, 0u, 0u, 0u);
+                if (g < groups && tile < tiles && r < rows) q[g] = load_scales(src + r * pitch, 4 * pair, KB, wide);
+            }
+        };
+        int it = 0;
+        if (pair0 < pair1) fetch(first, pair0, nxt);
+        for (int tile = first; tile < tiles && ok; tile += stride) {
+            for (int pair = pair0; pair < pair1 && ok; ++pair) {
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) cur[g] = nxt[g];
+                if (pair + 1 < pair1)
+                    fetch(tile, pair + 1, nxt);
+                else
+                    fetch(tile + stride, pair0, nxt);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (2 * pair + j >= k1) break;
+                    const int s = it % kStages;
+                    if (!(ok = tc5::mbar_wait(empty(s), (it / kStages & 1) ^ 1, abort))) break;
+                    uint8_t* at = smem + s * S::kStageBytes + (isW ? kOffWs : kOffAs);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int c = 0; c < (kGroups + 3) / 4; ++c) {
+                            if (4 * c >= groups) break;
+                            uint32_t w[4];
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const uint4 q = 4 * c + g < kGroups ? cur[4 * c + g < kGroups ? 4 * c + g : 0]
+                                                                    : make_uint4(0u, 0u, 0u, 0u);
+                                w[g] = j == 0 ? (h == 0 ? q.x : q.y) : (h == 0 ? q.z : q.w);
+                            }
+                            const int chunk = isW ? h : h * S::kTokChunks + c;
+                            reinterpret_cast<uint4*>(at + 512 * chunk)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    tc5::fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) tc5::mbar_arrive(full(s));
+                    ++it;
+                }
+            }
+        }
+        if (!ok) *abort = 1;
+    } else {
+        const int e = threadIdx.x - (kProdThreads - kEpiThreads);  // 0..255
+        const int quarter = warp & 3, half = (warp - 4) >> 2;      // lanes of tensor memory that a warp may read
+        const uint32_t row = (uint32_t)(32 * quarter) << 16;
+        int n = 0;
+        for (int tile = first; tile < tiles; tile += stride, ++n) {
+            const int a = n % S::kSums;
+            const int v0 = tile % p.chan_tiles * (kChan / 8);
+            const int64_t t0 = (int64_t)(tile / p.chan_tiles) * kTok;
+            if (kMix) {
+                // the streams of this tile towards L2, while its sums are made:
+                // 128-byte lines, two for each stream of a token
+                for (int i = e; i < kTok * 8; i += kEpiThreads) {
+                    const int64_t t = t0 + (i >> 3);
+                    const int v = v0 + (i & 1) * 8;
+                    if (t < p.T && 8 * v < p.N) prefetch_l2(p.X + (t * 4 + (i >> 1 & 3)) * (p.N >> 3) + v);
+                }
+            }
+            if (ok) ok = tc5::mbar_wait(sum_full(a), n / S::kSums & 1, abort);
+            __syncwarp();
+            tc5::fence_after_sync();
+            constexpr int kGroup = 32;  // tokens between two barriers of the epilogue
+#pragma unroll 1
+            for (int g = 0; g < kTok; g += kGroup) {
+                if (g + 16 * half < kTok) {
+                    float v[16];
+                    tc5::tmem_load16(tmem + row + a * kTok + g + 16 * half, v);
+                    // whole: two buffers in turn; split: each token in its place
+                    float* to = epi + ((S::kSplit ? g : g & kGroup) + 16 * half) * kChan + 32 * quarter + lane;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) to[i * kChan] = ok ? v[i] : __int_as_float(0x7fffffff);
+                }
+                if (!S::kSplit) {
+                    if (g + kGroup >= kTok) {  // the last read of this tile's sums
+                        tc5::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) tc5::mbar_arrive(sum_empty(a));
+                    }
+                    asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
+#pragma unroll
+                    for (int i = e; i < kGroup * (kChan / 8); i += kEpiThreads) {
+                        const int tok = i >> 4, v = i & 15;
+                        const int64_t t = t0 + g + tok;
+                        if (t < p.T && g + tok < kTok && 8 * (v0 + v) < p.N) {
+                            const float4* q = reinterpret_cast<const float4*>(epi + ((g & kGroup) + tok) * kChan) + 2 * v;
+                            const float4 lo = q[0], hi = q[1];
+                            const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                            emit<kMix>(p, f, t, v0 + v);
+                        }
+                    }
+                }
+            }
+        }
+        if (!ok) *abort = 1;
+    }
+    if (!ok) mx4_wait_expired = 1;
+    __syncwarp();
+
+    if (S::kSplit) {
+        // one tile a cluster: this CTA adds up its share of the tile's vectors
+        tc5::cluster_sync();
+        const int v0 = first % p.chan_tiles * (kChan / 8);
+        const int64_t t0 = (int64_t)(first / p.chan_tiles) * kTok;
+        constexpr int kItems = kTok * (kChan / 8);
+        for (int i = rank * kProdThreads + threadIdx.x; i < kItems; i += ranks * kProdThreads) {
+            const int tok = i >> 4, v = i & 15;
+            if (t0 + tok < p.T && 8 * (v0 + v) < p.N) {
+                float f[8] = {};
+                for (int r = 0; r < ranks; ++r) {
+                    const uint32_t at = tc5::map_rank(tc5::smem_addr(epi + tok * kChan + 8 * v), r);
+                    const float4 lo = tc5::load_cluster(at), hi = tc5::load_cluster(at + 16);
+                    const float q[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) f[x] += q[x];
+                }
+                emit<kMix>(p, f, t0 + tok, v0 + v);
+            }
+        }
+        tc5::cluster_sync();  // nobody's shared memory goes while it may be read
+    }
+    tc5::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc5::fence_after_sync();
+        tc5::tmem_free<S::kColumns>(tmem);
     }
 }
 
@@ -135,22 +446,119 @@ cudaError_t launch_premap_fwd_mx4(const uint16_t* X, const float* hpre, uint8_t*
     return cudaGetLastError();
 }
 
+namespace {
+
+// A byte matrix [rows][pitch] read in boxes of box_rows x 128 bytes.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled()
+{
+    static std::atomic<void*> kept{nullptr};  // the driver's function; the same for every device
+    void* f = kept.load(std::memory_order_acquire);
+    if (f == nullptr) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        kept.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+}
+
+bool code_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box_rows)
+{
+    const EncodeTiled f = encode_tiled();
+    const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(K / 2)};
+    const cuuint32_t box[2] = {kStepBytes, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return f != nullptr && f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box,
+                             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class S, bool kMix>
+cudaError_t product(const uint8_t* A, const uint8_t* W, ProductArgs p, cudaStream_t s)
+{
+    const auto kernel = mx4_product_kernel<S, kMix>;
+    static std::atomic<uint64_t> allowed{0};  // devices whose shared-memory limit is set for this kernel
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(allowed.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) allowed.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    }
+    p.chan_tiles = (p.N + kChan - 1) / kChan;
+    p.tok_tiles = (int)((p.T + S::kTok - 1) / S::kTok);
+    const int64_t tiles = (int64_t)p.chan_tiles * p.tok_tiles;
+    if (tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
+    CUtensorMap mapW, mapA;
+    if (!code_map(&mapW, W, p.N, p.K, kChan) || !code_map(&mapA, A, p.T, p.K, S::kTok)) return cudaErrorInvalidValue;
+
+    const int sms = device_sm_count(), pairs = (p.K / 2 + 2 * kStepBytes - 1) / (2 * kStepBytes);
+    int ranks = 1;
+    if (S::kSplit)  // CTAs that share a tile: as many as still fit the GPU, and have work
+        while (ranks < 8 && (ranks + 1) * tiles <= sms && ranks < pairs) ++ranks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(S::kSplit ? tiles * ranks : tiles < sms ? tiles : sms));
+    cfg.blockDim = dim3(kProdThreads);
+    cfg.dynamicSmemBytes = S::kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = S::kSplit ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, mapW, mapA, p);
+}
+
+using Split16 = ProductShape<16, 9, true>;
+using Split64 = ProductShape<64, 6, true>;
+using Whole192 = ProductShape<192, 4, false>;
+
+template <bool kMix>
+cudaError_t product_by_size(const uint8_t* A, const uint8_t* W, const ProductArgs& p, cudaStream_t s)
+{
+    if (p.T <= 16) return product<Split16, kMix>(A, W, p, s);
+    if (p.T <= 64) return product<Split64, kMix>(A, W, p, s);
+    return product<Whole192, kMix>(A, W, p, s);
+}
+
+}  // namespace
+
 cudaError_t launch_mx4_linear(const uint8_t* A, const uint8_t* As, const uint8_t* W, const uint8_t* Ws, uint16_t* out,
                               int64_t T, int64_t N, int64_t K, cudaStream_t s)
 {
-    const dim3 grid((unsigned)(N / 8), (unsigned)((T + kDotTokens - 1) / kDotTokens));
-    mx4_dot_kernel<false><<<grid, kDotThreads, 0, s>>>(A, As, W, Ws, MixArgs{}, (uint4*)out, T, (int)N, (int)K);
-    return cudaGetLastError();
+    return product_by_size<false>(
+        A, W, ProductArgs{As, Ws, (uint4*)out, nullptr, nullptr, nullptr, T, (int)N, (int)K, 0, 0}, s);
 }
 
 cudaError_t launch_mx4_linear_mix(const uint8_t* A, const uint8_t* As, const uint8_t* W, const uint8_t* Ws,
                                   const uint16_t* X, const float* H, const float* hpost, uint16_t* Y, int64_t T,
                                   int64_t C, int64_t K, cudaStream_t s)
 {
-    const dim3 grid((unsigned)(C / 8), (unsigned)((T + kDotTokens - 1) / kDotTokens));
-    mx4_dot_kernel<true><<<grid, kDotThreads, 0, s>>>(A, As, W, Ws, MixArgs{(const uint4*)X, H, hpost}, (uint4*)Y, T,
-                                                      (int)C, (int)K);
-    return cudaGetLastError();
+    return product_by_size<true>(
+        A, W, ProductArgs{As, Ws, (uint4*)Y, (const uint4*)X, H, hpost, T, (int)C, (int)K, 0, 0}, s);
+}
+
+// The status of the bounded waits since the last call (synchronises the device).
+cudaError_t read_wait_status(bool* expired)
+{
+    int v = 0;
+    const int zero = 0;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, mx4_wait_expired, sizeof v);
+    if (e == cudaSuccess && v != 0) e = cudaMemcpyToSymbol(mx4_wait_expired, &zero, sizeof zero);
+    *expired = v != 0;
+    return e;
 }
 
 }  // namespace mhc

@@ -473,6 +473,16 @@ MHC_API int mhc_mx4_linear_mix(const uint8_t *A_codes, const uint8_t *A_scales, 
                                const float *h_post, uint16_t *Y, int64_t T, int64_t C, int64_t K, void *stream);
 
 /*
+ * mhc_wait_status -- diagnostic of the products: their kernels hand tiles from
+ * one warp to another through waits that end after two seconds at most.  A
+ * wait that runs out means a fault of the device or a defect, not a bad
+ * argument; the outputs that were not done are NaN.  Returns MHC_ERR_CUDA if
+ * that happened on the current device since the last call, MHC_OK otherwise.
+ * Synchronises the device: not for use during stream capture.
+ */
+MHC_API int mhc_wait_status(void);
+
+/*
  * mhc_composite_gain -- diagnostic of the composite mixing map across depth:
  * per token, M = P_{L-1} ... P_1 P_0 (layer 0 applied first) and its largest
  * absolute row sum (forward signal gain) and column sum (gradient gain).
