@@ -125,25 +125,36 @@ struct ProductShape {
     static_assert(kSmemBytes > 116 * 1024 && kSmemBytes <= 227 * 1024, "shared memory");
 };
 
-// Four words of scales (two K tiles) of one row from word w0 on; words and
-// bytes past the row's blocks are zero.  wide: rows start on 16 bytes.
-__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int w0, int KB, bool wide)
+// The scales of a pair of K tiles (512 elements) of one row: 16 bytes, fetched
+// at once where rows start on 16 bytes (wide) and word by word where not
+// (words past the row read as zero).  Volatile, so that the loads stay where
+// they are issued, a round ahead of their use.
+__device__ __forceinline__ uint4 fetch_scales(const uint8_t* row, int pair, int pitch, bool wide)
 {
-    uint32_t w[4];
+    uint4 q;
     if (wide) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + 4 * w0));
-        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                     : "l"(row + 16 * pair));
     } else {
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = 4 * (w0 + j) < KB ? __ldg(reinterpret_cast<const uint32_t*>(row) + w0 + j) : 0u;
+        for (int j = 0; j < 4; ++j) {
+            const int at = 16 * pair + 4 * j;
+            w[j] = 0u;
+            if (at < pitch) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(w[j]) : "l"(row + at));
+        }
+        q = make_uint4(w[0], w[1], w[2], w[3]);
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int left = KB - 4 * (w0 + j);  // blocks that the word still holds
-        if (left < 4) w[j] = left <= 0 ? 0u : w[j] & (0xffffffffu >> (8 * (4 - left)));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return q;
+}
+
+// Word w of a row's scales without the bytes past its KB blocks: what lies
+// there meets code zeros, which a NaN scale would turn into NaN.
+__device__ __forceinline__ uint32_t scales_within(uint32_t word, int w, int KB)
+{
+    const int left = KB - 4 * w;
+    return left >= 4 ? word : left <= 0 ? 0u : word & (0xffffffffu >> (8 * (4 - left)));
 }
 
 // Eight channels of a token: vector v of N / 8.
@@ -297,29 +308,37 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         const int64_t rows = isW ? (int64_t)p.N : p.T;
         constexpr int kGroups = (kTok + 31) / 32 > 4 ? (kTok + 31) / 32 : 4;
         const int groups = isW ? 4 : (kTok + 31) / 32;
-        uint4 cur[kGroups], nxt[kGroups];
-        const auto fetch = [&](int tile, int pair, uint4(&q)[kGroups]) {
+        // two pairs of K tiles are in use while the next two are on their way
+        uint4 cur[2][kGroups], nxt[2][kGroups];
+        const auto fetch = [&](int tile, int pair) {
+            if (tile >= tiles) return;
             const int64_t r0 = isW ? (int64_t)(tile % p.chan_tiles) * kChan : (int64_t)(tile / p.chan_tiles) * kTok;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
-                const int64_t r = r0 + 32 * g + lane;
-                q[g] = make_uint4(0u, 0u, 0u, 0u);
-                if (g < groups && tile < tiles && r < rows) q[g] = load_scales(src + r * pitch, 4 * pair, KB, wide);
+                if (g >= groups) break;
+                // rows past the end stand in for none: what they give is not written
+                const uint8_t* row = src + min(r0 + 32 * g + lane, rows - 1) * pitch;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (pair + u < pair1) nxt[u][g] = fetch_scales(row, pair + u, pitch, wide);
             }
         };
         int it = 0;
-        if (pair0 < pair1) fetch(first, pair0, nxt);
+        fetch(first, pair0);
         for (int tile = first; tile < tiles && ok; tile += stride) {
-            for (int pair = pair0; pair < pair1 && ok; ++pair) {
+            for (int pair = pair0; pair < pair1 && ok; pair += 2) {
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) cur[g] = nxt[g];
-                if (pair + 1 < pair1)
-                    fetch(tile, pair + 1, nxt);
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) cur[u][g] = nxt[u][g];
+                if (pair + 2 < pair1)
+                    fetch(tile, pair + 2);
                 else
-                    fetch(tile + stride, pair0, nxt);
+                    fetch(tile + stride, pair0);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (2 * pair + j >= k1) break;
+                for (int j = 0; j < 4; ++j) {  // K tiles
+                    const int k = 2 * pair + j;
+                    if (k >= k1) break;
                     const int s = it % kStages;
                     if (!(ok = tc5::mbar_wait(empty(s), (it / kStages & 1) ^ 1, abort))) break;
                     uint8_t* at = smem + s * S::kStageBytes + (isW ? kOffWs : kOffAs);
@@ -331,9 +350,13 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                             uint32_t w[4];
 #pragma unroll
                             for (int g = 0; g < 4; ++g) {
-                                const uint4 q = 4 * c + g < kGroups ? cur[4 * c + g < kGroups ? 4 * c + g : 0]
-                                                                    : make_uint4(0u, 0u, 0u, 0u);
-                                w[g] = j == 0 ? (h == 0 ? q.x : q.y) : (h == 0 ? q.z : q.w);
+                                const int r = 4 * c + g;
+                                w[g] = 0u;
+                                if (r < kGroups && r < groups) {
+                                    const uint4 q = cur[j >> 1][r < kGroups ? r : 0];
+                                    w[g] = (j & 1) == 0 ? (h == 0 ? q.x : q.y) : (h == 0 ? q.z : q.w);
+                                }
+                                if (8 * (k + 1) > KB) w[g] = scales_within(w[g], 2 * k + h, KB);
                             }
                             const int chunk = isW ? h : h * S::kTokChunks + c;
                             reinterpret_cast<uint4*>(at + 512 * chunk)[lane] = make_uint4(w[0], w[1], w[2], w[3]);

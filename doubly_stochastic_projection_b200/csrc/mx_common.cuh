@@ -92,43 +92,38 @@ __device__ __forceinline__ uint2 mx_encode8(const float (&f)[8], int S)
 {
     if (S == kMxScaleNaN) return make_uint2(0u, 0u);
     const float inv = mx_inverse_scale(S);
-    if (kFmt == MHC_MX_INT8) {
-        uint32_t w[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t b[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // the sum with 1.5 * 2^23 rounds 64 q to an integer, ties to
-                // even, into the low bits; only S = 254 can leave |64 q| above 127
-                float q = f[4 * h + e] * inv;
-                if (S == 254) q = fminf(fmaxf(q, -1.984375f), 1.984375f);
-                b[e] = __float_as_uint(fmaf(q, 64.0f, 12582912.0f));
-            }
-            w[h] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-        }
-        return make_uint2(w[0], w[1]);
-    }
     float q[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) q[e] = f[e] * inv;
-    if (kFmt == MHC_MX_E4M3) {
+    if constexpr (kFmt == MHC_MX_INT8) {
+        uint32_t b[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            // the sum with 1.5 * 2^23 rounds 64 q to an integer, ties to even,
+            // into the low bits; only S = 254 can leave |64 q| above 127
+            if (S == 254) q[e] = fminf(fmaxf(q[e], -1.984375f), 1.984375f);
+            b[e] = __float_as_uint(fmaf(q[e], 64.0f, 12582912.0f));
+        }
+        return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                          __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+    } else if constexpr (kFmt == MHC_MX_E4M3) {
         uint16_t p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p[e]) : "f"(q[2 * e + 1]), "f"(q[2 * e]));
         return make_uint2((uint32_t)p[0] | (uint32_t)p[1] << 16, (uint32_t)p[2] | (uint32_t)p[3] << 16);
+    } else {
+        uint32_t w;
+        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+            "mov.b32 %0, {a, b, c, d};\n\t}"
+            : "=r"(w)
+            : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+        return make_uint2(w, 0u);
     }
-    uint32_t w;
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-        "mov.b32 %0, {a, b, c, d};\n\t}"
-        : "=r"(w)
-        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-    return make_uint2(w, 0u);
 }
 
 __device__ __forceinline__ void mx_half2_to_float(uint32_t h, float& lo, float& hi)
