@@ -64,14 +64,14 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 // tile of 128 channels (the rows of tensor memory) by kTok tokens (its
 // columns) and walks K in tiles of 256 elements, 128 bytes a row.  Its warps:
 //   0     loads the code tiles by TMA (128-byte swizzle) into a ring of stages
-//   1     issues the tcgen05 instructions: scales into tensor memory, four
-//         steps of 64 a tile
+//   1     issues the products, four steps of 64 a tile
 //   2, 3  bring the scales of W and A.  They are rows of bytes in memory and
 //         have to be, for the tensor cores, chunks of 512 bytes with the four
 //         bytes of rows r, r + 32, r + 64, r + 96 side by side: a lane reads 16
 //         bytes (two tiles' worth) of four rows and stores four 16-byte vectors
 //   4-11  the epilogue: tensor memory -> shared memory, turned so that a
 //         thread holds eight consecutive channels of a token -> the output
+//   12    issues the copies of the scales into tensor memory
 // Two forms.  Whole: one persistent CTA an SM walks output tiles, the sums of
 // one tile in one half of tensor memory while the epilogue drains the other.
 // Split: a cluster shares one output tile, each CTA a part of K; the partial
@@ -83,7 +83,7 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 
 constexpr int kChan = 128;      // channels of a tile
 constexpr int kStepBytes = 128; // bytes of K of a tile: 256 elements
-constexpr int kProdThreads = 384;
+constexpr int kProdThreads = 416;  // 13 warps, four on one scheduler: 128 registers a thread at most
 constexpr int kEpiWarps = 8;
 constexpr int kEpiThreads = 32 * kEpiWarps;
 
@@ -107,13 +107,15 @@ struct ProductShape {
     static constexpr bool kSplit = kSplit_;
     static constexpr int kTokChunks = (kTok + 127) / 128;  // 128-row chunks of A's scales
     static constexpr int kWBytes = kChan * kStepBytes, kABytes = kTok * kStepBytes;
-    static constexpr int kWsBytes = 2 * 512, kAsBytes = 2 * kTokChunks * 512;
-    static constexpr int kStageBytes = kWBytes + kABytes + kWsBytes + kAsBytes;
+    static constexpr int kStageBytes = kWBytes + kABytes;
+    // scales: two buffers of four K tiles, a tile's being two halves (of 128
+    // elements) of one chunk of W's and kTokChunks of A's
+    static constexpr int kScaleTile = 2 * 512 * (1 + kTokChunks), kScaleBytes = 2 * 4 * kScaleTile;
     static constexpr int kSums = kSplit ? 1 : 2;  // accumulator tiles
     // the epilogue's: two buffers of 32 tokens, or the whole tile's partial sums
     static constexpr int kEpiBytes = (kSplit ? kTok : 64) * kChan * 4;
-    static constexpr int kBars = 2 * kStages + 2 * kSums + 1;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + 8 * kBars + 16;
+    static constexpr int kBars = 2 * kStages + 4 + 2 * kSums + 1;
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kScaleBytes + kEpiBytes + 8 * kBars + 16;
     // columns of tensor memory: sums, then each stage's scales of W and A
     static constexpr int kScaleCols = 8 + 8 * kTokChunks;
     static constexpr int kSumCols = (kSums * kTok + 31) / 32 * 32;
@@ -196,31 +198,40 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
     constexpr int kTok = S::kTok, kStages = S::kStages;
     const uint32_t base = (tc5::smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - tc5::smem_addr(smem_raw));
-    float* epi = reinterpret_cast<float*>(smem + kStages * S::kStageBytes);
-    const uint32_t bars = base + kStages * S::kStageBytes + S::kEpiBytes;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kStages * S::kStageBytes + S::kEpiBytes + 8 * S::kBars);
+    constexpr int kOffScales = kStages * S::kStageBytes, kOffEpi = kOffScales + S::kScaleBytes,
+                  kOffBars = kOffEpi + S::kEpiBytes;
+    float* epi = reinterpret_cast<float*>(smem + kOffEpi);
+    const uint32_t bars = base + kOffBars;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBars + 8 * S::kBars);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const auto full = [&](int s) { return bars + 8 * s; };
     const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
-    const auto sum_full = [&](int a) { return bars + 8 * (2 * kStages + a); };
-    const auto sum_empty = [&](int a) { return bars + 8 * (2 * kStages + S::kSums + a); };
-    const uint32_t drained = bars + 8 * (2 * kStages + 2 * S::kSums);  // used when a wait has run out
-    // offsets within a stage: W, A, scales of W, scales of A
-    constexpr int kOffA = S::kWBytes, kOffWs = kOffA + S::kABytes, kOffAs = kOffWs + S::kWsBytes;
+    const auto scales_full = [&](int b) { return bars + 8 * (2 * kStages + b); };
+    const auto scales_empty = [&](int b) { return bars + 8 * (2 * kStages + 2 + b); };
+    const auto sum_full = [&](int a) { return bars + 8 * (2 * kStages + 4 + a); };
+    const auto sum_empty = [&](int a) { return bars + 8 * (2 * kStages + 4 + S::kSums + a); };
+    const uint32_t drained = bars + 8 * (2 * kStages + 4 + 2 * S::kSums);  // used when a wait has run out
+    constexpr int kOffA = S::kWBytes;  // within a stage
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // shuffled: uniform for the compiler too, which halves the cost of issuing a
+    // tensor instruction (0.7 of it in moves to uniform registers otherwise)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (warp == 0 && lane == 0) {
         tc5::prefetch_map(&mapW);
         tc5::prefetch_map(&mapA);
         for (int s = 0; s < kStages; ++s) {
-            tc5::mbar_init(full(s), 3);  // the TMA thread and two scale warps
+            tc5::mbar_init(full(s), 2);  // the codes by TMA, the scales by tensor copy
             tc5::mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc5::mbar_init(scales_full(b), 2);  // the two scale warps
+            tc5::mbar_init(scales_empty(b), 1);
         }
         for (int a = 0; a < S::kSums; ++a) {
             tc5::mbar_init(sum_full(a), 1);
             tc5::mbar_init(sum_empty(a), kEpiWarps);
         }
-        tc5::mbar_init(drained, 1);
+        tc5::mbar_init(drained, 2);
         *abort = 0;
         tc5::fence_mbar_init();
     }
@@ -228,7 +239,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
     tc5::fence_before_sync();
     __syncthreads();
     tc5::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     pdl_wait();
 
     // this CTA's output tiles, and its share of K in pairs of tiles
@@ -240,64 +251,98 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
     const int first = blockIdx.x / ranks, stride = gridDim.x / ranks;
     bool ok = true;
 
+    const int mine = first < tiles ? (tiles - 1 - first) / stride + 1 : 0, steps = k1 - k0;  // output tiles, K tiles
     if (warp == 0) {
-        if (lane == 0) {
-            int it = 0;
-            for (int tile = first; tile < tiles && ok; tile += stride) {
-                const int n0 = tile % p.chan_tiles * kChan, t0 = tile / p.chan_tiles * kTok;
-                for (int k = k0; k < k1; ++k, ++it) {
-                    const int s = it % kStages;
-                    if (!(ok = tc5::mbar_wait(empty(s), (it / kStages & 1) ^ 1, abort))) break;
-                    const uint32_t at = base + s * S::kStageBytes;
+        int s = 0, t = first;
+        uint32_t phase = 0;
+        int64_t loads = 0;
+        for (int n = 0; n < mine && ok; ++n, t += stride) {
+            const int n0 = t % p.chan_tiles * kChan, t0 = t / p.chan_tiles * kTok;
+            for (int k = k0; k < k1; ++k, ++loads) {
+                if (!(ok = tc5::mbar_wait_warp(empty(s), phase ^ 1, abort))) break;
+                const uint32_t at = base + s * S::kStageBytes;
+                if (tc5::elect_one()) {
                     tc5::mbar_expect_tx(full(s), S::kWBytes + S::kABytes);
                     tc5::tma_load_2d(at, &mapW, k * kStepBytes, n0, full(s));
                     tc5::tma_load_2d(at + kOffA, &mapA, k * kStepBytes, t0, full(s));
                 }
-            }
-            if (!ok) {
-                // the copies in flight: the last kStages ones at most
-                *abort = 1;
-                for (int j = max(0, it - kStages); j < it; ++j)
-                    tc5::mbar_wait(full(j % kStages), j / kStages & 1, nullptr, kDrainNs);
+                __syncwarp();
+                s = s + 1 == kStages ? 0 : s + 1;
+                phase ^= s == 0;
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t inst = tc5::mx4_instruction(kChan, kTok);
-            int it = 0, n = 0;
-            for (int tile = first; tile < tiles && ok; tile += stride, ++n) {
-                const int a = n % S::kSums;
-                if (!(ok = tc5::mbar_wait(sum_empty(a), (n / S::kSums & 1) ^ 1, abort))) break;
+        if (!ok) {
+            *abort = 1;  // the copies in flight: the last kStages at most
+            for (int64_t j = loads > kStages ? loads - kStages : 0; j < loads; ++j)
+                tc5::mbar_wait(full((int)(j % kStages)), (uint32_t)(j / kStages) & 1, nullptr, kDrainNs);
+        }
+    } else if (warp == 12) {
+        // each K tile's scales from shared into tensor memory, ahead of the products
+        int s = 0, buf = 0;
+        uint32_t phase = 0, par = 0;
+        for (int n = 0; n < mine && ok; ++n) {
+            for (int k = 0; k < steps; ++k) {
+                if ((k & 3) == 0 && !(ok = tc5::mbar_wait_warp(scales_full(buf), par, abort))) break;
+                if (!(ok = tc5::mbar_wait_warp(empty(s), phase ^ 1, abort))) break;
                 tc5::fence_after_sync();
-                const uint32_t d = tmem + a * kTok;
-                for (int k = k0; k < k1; ++k, ++it) {
-                    const int s = it % kStages;
-                    if (!(ok = tc5::mbar_wait(full(s), it / kStages & 1, abort))) break;
-                    tc5::fence_after_sync();
-                    const uint32_t at = base + s * S::kStageBytes;
-                    const uint32_t sw = tmem + S::kSumCols + s * S::kScaleCols, sa = sw + 8;
+                const uint32_t at = base + kOffScales + (buf * 4 + (k & 3)) * S::kScaleTile;
+                const uint32_t sw = tmem + S::kSumCols + s * S::kScaleCols;
+                const bool last = (k & 3) == 3 || k + 1 == steps;  // of this buffer
+                if (tc5::elect_one()) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tc5::copy_scales(sw + 4 * h, tc5::scale_desc(at + kOffWs + 512 * h));
-#pragma unroll
-                        for (int c = 0; c < S::kTokChunks; ++c)
-                            tc5::copy_scales(sa + 4 * (h * S::kTokChunks + c),
-                                             tc5::scale_desc(at + kOffAs + 512 * (h * S::kTokChunks + c)));
-                    }
-                    const uint64_t dw = tc5::operand_desc(at), da = tc5::operand_desc(at + kOffA);
+                    for (int c = 0; c < 2 * (1 + S::kTokChunks); ++c)
+                        tc5::copy_scales(sw + 4 * c, tc5::scale_desc(at + 512 * c));
+                    tc5::commit(full(s));
+                    if (last) tc5::commit(scales_empty(buf));
+                }
+                __syncwarp();
+                s = s + 1 == kStages ? 0 : s + 1;
+                phase ^= s == 0;
+                buf ^= last;
+                par ^= last && buf == 0;
+            }
+        }
+        if (!ok) {
+            *abort = 1;
+            if (tc5::elect_one()) tc5::commit(drained);
+            __syncwarp();
+            tc5::mbar_wait(drained, 0, nullptr, kDrainNs);
+        }
+    } else if (warp == 1) {
+        // The whole warp waits, one lane issues.  The queue behind it is short
+        // (a delay of some 150 cycles between two K tiles is hidden, one of 250 is
+        // not), so nothing else is done here.
+        constexpr uint32_t inst = tc5::mx4_instruction(kChan, kTok);
+        int s = 0;
+        uint32_t phase = 0;
+        for (int n = 0; n < mine && ok; ++n) {
+            const int a = n % S::kSums;
+            if (!(ok = tc5::mbar_wait_warp(sum_empty(a), (n / S::kSums & 1) ^ 1, abort))) break;
+            const uint32_t d = tmem + a * kTok;
+            for (int k = 0; k < steps; ++k) {
+                if (!(ok = tc5::mbar_wait_warp(full(s), phase, abort))) break;
+                tc5::fence_after_sync();
+                const uint32_t at = base + s * S::kStageBytes;
+                const uint32_t sw = tmem + S::kSumCols + s * S::kScaleCols, sa = sw + 8;
+                const uint64_t dw = tc5::operand_desc(at), da = tc5::operand_desc(at + kOffA);
+                if (tc5::elect_one()) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)  // 64 elements: 32 bytes along the swizzled row
                         tc5::mma_mx4(d, dw + 2 * q, da + 2 * q, inst | tc5::scale_select(2 * (q & 1)), sw + 4 * (q >> 1),
-                                     sa + 4 * S::kTokChunks * (q >> 1), k > k0 || q > 0);
+                                     sa + 4 * S::kTokChunks * (q >> 1), k > 0 || q > 0);
                     tc5::commit(empty(s));
+                    if (k + 1 == steps) tc5::commit(sum_full(a));
                 }
-                if (ok) tc5::commit(sum_full(a));
+                __syncwarp();
+                s = s + 1 == kStages ? 0 : s + 1;
+                phase ^= s == 0;
             }
-            if (!ok) {
-                *abort = 1;  // the tensor work in flight, before its memory is freed
-                tc5::commit(drained);
-                tc5::mbar_wait(drained, 0, nullptr, kDrainNs);
-            }
+        }
+        if (!ok) {
+            *abort = 1;  // the tensor work in flight, before its memory is freed
+            if (tc5::elect_one()) tc5::commit(drained);
+            __syncwarp();
+            tc5::mbar_wait(drained, 0, nullptr, kDrainNs);
         }
     } else if (warp < 4) {
         // warp 2: W's rows, warp 3: A's; lane l holds rows l, l + 32, ... of the tile
@@ -308,8 +353,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         const int64_t rows = isW ? (int64_t)p.N : p.T;
         constexpr int kGroups = (kTok + 31) / 32 > 4 ? (kTok + 31) / 32 : 4;
         const int groups = isW ? 4 : (kTok + 31) / 32;
-        // two pairs of K tiles are in use while the next two are on their way
-        uint4 cur[2][kGroups], nxt[2][kGroups];
+        // two pairs of K tiles, fetched while the buffers before them are in work
+        uint4 next[2][kGroups];
         const auto fetch = [&](int tile, int pair) {
             if (tile >= tiles) return;
             const int64_t r0 = isW ? (int64_t)(tile % p.chan_tiles) * kChan : (int64_t)(tile / p.chan_tiles) * kTok;
@@ -320,28 +365,20 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 const uint8_t* row = src + min(r0 + 32 * g + lane, rows - 1) * pitch;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
-                    if (pair + u < pair1) nxt[u][g] = fetch_scales(row, pair + u, pitch, wide);
+                    if (pair + u < pair1) next[u][g] = fetch_scales(row, pair + u, pitch, wide);
             }
         };
-        int it = 0;
+        int buf = 0;
+        uint32_t par = 0;
         fetch(first, pair0);
         for (int tile = first; tile < tiles && ok; tile += stride) {
             for (int pair = pair0; pair < pair1 && ok; pair += 2) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) cur[u][g] = nxt[u][g];
-                if (pair + 2 < pair1)
-                    fetch(tile, pair + 2);
-                else
-                    fetch(tile + stride, pair0);
+                if (!(ok = tc5::mbar_wait(scales_empty(buf), par ^ 1, abort))) break;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {  // K tiles
                     const int k = 2 * pair + j;
                     if (k >= k1) break;
-                    const int s = it % kStages;
-                    if (!(ok = tc5::mbar_wait(empty(s), (it / kStages & 1) ^ 1, abort))) break;
-                    uint8_t* at = smem + s * S::kStageBytes + (isW ? kOffWs : kOffAs);
+                    uint8_t* at = smem + kOffScales + (buf * 4 + j) * S::kScaleTile + (isW ? 0 : 1024);
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -353,7 +390,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                                 const int r = 4 * c + g;
                                 w[g] = 0u;
                                 if (r < kGroups && r < groups) {
-                                    const uint4 q = cur[j >> 1][r < kGroups ? r : 0];
+                                    const uint4 q = next[j >> 1][r < kGroups ? r : 0];
                                     w[g] = (j & 1) == 0 ? (h == 0 ? q.x : q.y) : (h == 0 ? q.z : q.w);
                                 }
                                 if (8 * (k + 1) > KB) w[g] = scales_within(w[g], 2 * k + h, KB);
@@ -361,16 +398,21 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                             const int chunk = isW ? h : h * S::kTokChunks + c;
                             reinterpret_cast<uint4*>(at + 512 * chunk)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                    tc5::fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) tc5::mbar_arrive(full(s));
-                    ++it;
                 }
+                tc5::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) tc5::mbar_arrive(scales_full(buf));
+                if (pair + 2 < pair1)
+                    fetch(tile, pair + 2);
+                else
+                    fetch(tile + stride, pair0);
+                buf ^= 1;
+                par ^= buf == 0;
             }
         }
         if (!ok) *abort = 1;
     } else {
-        const int e = threadIdx.x - (kProdThreads - kEpiThreads);  // 0..255
+        const int e = threadIdx.x - 128;  // 0..255
         const int quarter = warp & 3, half = (warp - 4) >> 2;      // lanes of tensor memory that a warp may read
         const uint32_t row = (uint32_t)(32 * quarter) << 16;
         int n = 0;

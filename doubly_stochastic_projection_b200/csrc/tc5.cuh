@@ -59,6 +59,25 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return true;
 }
 
+// The same for a whole warp; the answer is the warp's, and the compiler knows
+// it, so the operands of tensor instructions stay in uniform registers in the
+// code that follows.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort)
+{
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
+// One lane of a whole warp.  Written as a predicate around single
+// instructions, it leaves the code around them warp-uniform, which the tensor
+// instructions' operands have to be.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // Makes this thread's shared-memory writes visible to TMA and tcgen05.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void fence_mbar_init()
