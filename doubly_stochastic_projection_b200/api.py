@@ -46,6 +46,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load the CUDA library (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:  # set once, whole
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB_PATH
@@ -118,6 +120,9 @@ def _stream(t) -> ctypes.c_void_p:
 
 
 def _need(t, name, dtype, shape=None):
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous() and \
+            (shape is None or t.shape == shape):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
@@ -126,7 +131,7 @@ def _need(t, name, dtype, shape=None):
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     return t
 
@@ -502,49 +507,58 @@ def _mx_format(fmt, allowed=("int8", "e4m3", "e2m1")):
     return _MX_FORMATS[fmt]
 
 
-def _mx_empty(shape, fmt, device):
+def _mx_empty(like, shape, fmt):
+    """An unwritten MxTensor of `shape` beside a tensor."""
     C = shape[-1]
-    codes = torch.empty(shape[:-1] + ((C // 2) if fmt == "e2m1" else C,), dtype=torch.uint8, device=device)
-    return MxTensor(codes, torch.empty(shape[:-1] + (mx_scale_pitch(C),), dtype=torch.uint8, device=device), fmt)
+    rows = tuple(shape[:-1])
+    if fmt == "e2m1":
+        codes = like.new_empty(rows + (C // 2,), dtype=torch.uint8)
+    elif like.shape == shape:
+        codes = torch.empty_like(like, dtype=torch.uint8)
+    else:
+        codes = like.new_empty(shape, dtype=torch.uint8)
+    return MxTensor(codes, like.new_empty(rows + (4 * ((C + 127) // 128),), dtype=torch.uint8), fmt)
 
 
 def _need_mx(mx, name, allowed, shape=None):
     """Checks a MxTensor and returns the shape that it stands for."""
     if not isinstance(mx, MxTensor):
         raise TypeError("%s must be an MxTensor" % name)
-    _mx_format(mx.fmt, allowed)
-    _need(mx.codes, name + ".codes", torch.uint8)
-    if mx.codes.dim() < 1:
+    codes, scales, fmt = mx
+    if fmt not in allowed:
+        _mx_format(fmt, allowed)
+    _need(codes, name + ".codes", torch.uint8)
+    s = tuple(codes.shape)
+    if not s:
         raise ValueError("%s.codes must have at least one dimension" % name)
-    s = tuple(mx.shape)
-    if shape is not None and s != tuple(shape):
+    if fmt == "e2m1":
+        s = s[:-1] + (2 * s[-1],)
+    if shape is not None and s != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), s))
-    _need(mx.scales, name + ".scales", torch.uint8, s[:-1] + (mx_scale_pitch(s[-1]),))
+    _need(scales, name + ".scales", torch.uint8, s[:-1] + (mx_scale_pitch(s[-1]),))
     return s
 
 
 _CKPT_FORMATS = ("int8", "e4m3")
 
 
-def _launch(f, *args):
-    """Calls entry point f on the current stream of its tensors' device, which must
-    be one and the same; the device is made current for the launch."""
-    dev = None
-    ptrs = []
-    for a in args:
-        if isinstance(a, torch.Tensor):
-            if dev is None:
-                dev = a.device
-            elif a.device != dev:
-                raise ValueError("tensors are on %s and %s" % (dev, a.device))
-            ptrs.append(a.data_ptr())
-        else:
-            ptrs.append(a)
-    if dev.index == torch.cuda.current_device():
-        rc = f(*ptrs, torch.cuda.current_stream(dev).cuda_stream)
+def _launch(f, tensors, *numbers):
+    """Calls entry point f with the tensors' pointers (None for those left out) and
+    the numbers, on the current stream of the tensors' device: they must share
+    one, which is made current for the launch if it is not."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors are on %s and %s" % (tensors[0].device, t.device))
+    ptrs = [None if t is None else t.data_ptr() for t in tensors]
+    # the handle behind torch.cuda.current_stream(dev).cuda_stream, without the
+    # Stream object: small calls are bound by this thread
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch.cuda.current_device():
+        rc = f(*ptrs, *numbers, stream)
     else:
         with torch.cuda.device(dev):
-            rc = f(*ptrs, torch.cuda.current_stream(dev).cuda_stream)
+            rc = f(*ptrs, *numbers, stream)
     if rc != 0:
         _check(rc)
 
@@ -561,10 +575,10 @@ def mx_pack(x, fmt, out: MxTensor | None = None) -> MxTensor:
     shape = tuple(x.shape)
     C = shape[-1]
     if out is None:
-        out = _mx_empty(shape, fmt, x.device)
+        out = _mx_empty(x, shape, fmt)
     else:
         _need_mx(out, "out", (fmt,), shape)
-    _launch(lib().mhc_mx_pack, x, out.codes, out.scales, x.numel() // C if C else 0, C, f)
+    _launch(lib().mhc_mx_pack, (x, out.codes, out.scales), x.numel() // C if C else 0, C, f)
     return out
 
 
@@ -573,9 +587,10 @@ def mx_unpack(mx: MxTensor, out=None):
     shape = _need_mx(mx, "mx", tuple(_MX_FORMATS))
     C = shape[-1]
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=mx.codes.device)
-    _need(out, "out", torch.bfloat16, shape)
-    _launch(lib().mhc_mx_unpack, mx.codes, mx.scales, out, out.numel() // C if C else 0, C, _MX_FORMATS[mx.fmt])
+        out = mx.codes.new_empty(shape, dtype=torch.bfloat16)
+    else:
+        _need(out, "out", torch.bfloat16, shape)
+    _launch(lib().mhc_mx_unpack, (mx.codes, mx.scales, out), out.numel() // C if C else 0, C, _MX_FORMATS[mx.fmt])
     return out
 
 
@@ -587,8 +602,8 @@ def residual_mix_fwd_ckpt(X, H_res, h_post, F, fmt="int8", out=None):
     _need(H_res, "H_res", torch.float32, (T, 4, 4))
     _need(h_post, "h_post", torch.float32, (T, 4))
     Y = torch.empty_like(X) if out is None else _need(out, "out", torch.bfloat16, X.shape)
-    Xq, Fq = _mx_empty((T, 4, C), fmt, X.device), _mx_empty((T, C), fmt, X.device)
-    _launch(lib().mhc_residual_mix_fwd_ckpt, X, H_res, h_post, F, Y, Xq.codes, Xq.scales, Fq.codes, Fq.scales, T, C, f)
+    Xq, Fq = _mx_empty(X, (T, 4, C), fmt), _mx_empty(F, (T, C), fmt)
+    _launch(lib().mhc_residual_mix_fwd_ckpt, (X, H_res, h_post, F, Y, *Xq[:2], *Fq[:2]), T, C, f)
     return Y, Xq, Fq
 
 
@@ -601,9 +616,8 @@ def proj_mix_fwd_ckpt(logits, h_post, X, F, fmt="int8", iters: int = 0, out=None
     _need(h_post, "h_post", torch.float32, (T, 4))
     Y = torch.empty_like(X) if out is None else _need(out, "out", torch.bfloat16, X.shape)
     H = torch.empty_like(logits)
-    Xq, Fq = _mx_empty((T, 4, C), fmt, X.device), _mx_empty((T, C), fmt, X.device)
-    _launch(lib().mhc_proj_mix_fwd_ckpt, logits, h_post, X, F, Y, H, Xq.codes, Xq.scales, Fq.codes, Fq.scales, T, C,
-            int(iters), f)
+    Xq, Fq = _mx_empty(X, (T, 4, C), fmt), _mx_empty(F, (T, C), fmt)
+    _launch(lib().mhc_proj_mix_fwd_ckpt, (logits, h_post, X, F, Y, H, *Xq[:2], *Fq[:2]), T, C, int(iters), f)
     return Y, H, Xq, Fq
 
 
@@ -631,12 +645,12 @@ def residual_mix_bwd_ckpt(Xq: MxTensor, H_res, h_post, Fq: MxTensor, dY, need_dH
     _need(H_res, "H_res", torch.float32, (T, 4, 4))
     _need(h_post, "h_post", torch.float32, (T, 4))
     dX = torch.empty_like(dY)
-    dF = torch.empty((T, C), dtype=torch.bfloat16, device=dY.device)
+    dF = dY.new_empty((T, C))
     dH = torch.empty_like(H_res) if need_dH else None
     dh = torch.empty_like(h_post) if need_dh_post else None
     dl = torch.empty_like(H_res) if need_dlogits else None
-    _launch(lib().mhc_residual_mix_bwd_ckpt, Xq.codes, Xq.scales, H_res, h_post, Fq.codes, Fq.scales, dY, dX, dH, dh,
-            dF, dl, T, C, _MX_FORMATS[Xq.fmt])
+    _launch(lib().mhc_residual_mix_bwd_ckpt, (*Xq[:2], H_res, h_post, *Fq[:2], dY, dX, dH, dh, dF, dl), T, C,
+            _MX_FORMATS[Xq.fmt])
     return {"dX": dX, "dF": dF, "dH_res": dH, "dh_post": dh, "dlogits": dl}
 
 
@@ -652,9 +666,9 @@ def mix_post_bwd_ckpt(dY, Fq: MxTensor, h_post):
     T, C = _streams_shape(dY, "dY")
     _need_mx(Fq, "Fq", _CKPT_FORMATS, (T, C))
     _need(h_post, "h_post", torch.float32, (T, 4))
-    dF = torch.empty((T, C), dtype=torch.bfloat16, device=dY.device)
+    dF = dY.new_empty((T, C))
     dh = torch.empty_like(h_post)
-    _launch(lib().mhc_mix_post_bwd_ckpt, dY, Fq.codes, Fq.scales, h_post, dF, dh, T, C, _MX_FORMATS[Fq.fmt])
+    _launch(lib().mhc_mix_post_bwd_ckpt, (dY, *Fq[:2], h_post, dF, dh), T, C, _MX_FORMATS[Fq.fmt])
     return dF, dh
 
 
@@ -670,7 +684,7 @@ def mix_premap_bwd_ckpt(Xq: MxTensor, H_res, h_pre, dY, dx_in, need_dH=False, ne
     dhp = torch.empty_like(h_pre)
     dH = torch.empty_like(H_res) if need_dH else None
     dl = torch.empty_like(H_res) if need_dlogits else None
-    _launch(lib().mhc_mix_premap_bwd_ckpt, Xq.codes, Xq.scales, H_res, h_pre, dY, dx_in, dX, dH, dhp, dl, T, C,
+    _launch(lib().mhc_mix_premap_bwd_ckpt, (*Xq[:2], H_res, h_pre, dY, dx_in, dX, dH, dhp, dl), T, C,
             _MX_FORMATS[Xq.fmt])
     return {"dX": dX, "dh_pre": dhp, "dH_res": dH, "dlogits": dl}
 
@@ -681,8 +695,8 @@ def premap_fwd_mx4(X, h_pre) -> MxTensor:
     _need(X, "X", torch.bfloat16)
     T, C = _streams_shape(X, "X")
     _need(h_pre, "h_pre", torch.float32, (T, 4))
-    out = _mx_empty((T, C), "e2m1", X.device)
-    _launch(lib().mhc_premap_fwd_mx4, X, h_pre, out.codes, out.scales, T, C)
+    out = _mx_empty(X, (T, C), "e2m1")
+    _launch(lib().mhc_premap_fwd_mx4, (X, h_pre, *out[:2]), T, C)
     return out
 
 
@@ -699,9 +713,10 @@ def mx4_linear(a: MxTensor, w: MxTensor, out=None):
     gradient."""
     T, N, K = _product_shapes(a, w)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=a.codes.device)
-    _need(out, "out", torch.bfloat16, (T, N))
-    _launch(lib().mhc_mx4_linear, a.codes, a.scales, w.codes, w.scales, out, T, N, K)
+        out = a.codes.new_empty((T, N), dtype=torch.bfloat16)
+    else:
+        _need(out, "out", torch.bfloat16, (T, N))
+    _launch(lib().mhc_mx4_linear, (*a[:2], *w[:2], out), T, N, K)
     return out
 
 
@@ -714,8 +729,9 @@ def mx4_linear_mix(a: MxTensor, w: MxTensor, X, H_res, h_post, out=None):
     _need(h_post, "h_post", torch.float32, (T, 4))
     if out is None:
         out = torch.empty_like(X)
-    _need(out, "out", torch.bfloat16, X.shape)
-    _launch(lib().mhc_mx4_linear_mix, a.codes, a.scales, w.codes, w.scales, X, H_res, h_post, out, T, C, K)
+    else:
+        _need(out, "out", torch.bfloat16, X.shape)
+    _launch(lib().mhc_mx4_linear_mix, (*a[:2], *w[:2], X, H_res, h_post, out), T, C, K)
     return out
 
 
