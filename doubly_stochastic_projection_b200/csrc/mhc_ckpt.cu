@@ -96,27 +96,40 @@ struct CkptOut {
     uint8_t *Xc, *Xs, *Fc, *Fs;
 };
 
+// The inputs come through the backward's prefetch ring (BwdRing in
+// mix_common.cuh: its four dY rows are X's here, its Z row is F), two vectors
+// ahead and across token boundaries: the arithmetic between a load and its
+// stores is long, and with loads straight into registers the kernel ran at
+// 62% of the copy bandwidth.
+constexpr int kFwdStages = 3;
+using FwdRing = BwdRing<kFwdStages, kThreads, false>;
+
 // Streams token t: X, F -> Y and the codes of X and F.
 template <int kFmt>
-__device__ __forceinline__ void mix_token_fwd_ckpt(const float (&h)[16], const float (&hp)[4], const uint4* X,
-                                                   const uint4* F, uint4* Y, const CkptOut& o, int64_t t, int CV)
+__device__ __forceinline__ void mix_token_fwd_ckpt(const float (&h)[16], const float (&hp)[4], FwdRing& ring, uint4* Y,
+                                                   const CkptOut& o, int64_t t, int CV)
 {
     const int64_t C = (int64_t)CV * 8, sp = mx_scale_pitch(C);
-    const uint4* Xt = X + t * 4 * CV;
     uint4* Yt = Y + t * 4 * CV;
     // the bound depends on the warp only: every lane takes part in the shuffles
     for (int v = threadIdx.x; (v & ~31) < CV; v += kThreads) {
         const bool in = v < CV;
-        uint4 r[5], y[4];
+        uint4 r[5];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[j] = in ? __ldcs(Xt + (int64_t)j * CV + v) : make_uint4(0u, 0u, 0u, 0u);
-        r[4] = in ? __ldcs(F + t * CV + v) : make_uint4(0u, 0u, 0u, 0u);
-        const uint4 x[4] = {r[0], r[1], r[2], r[3]};
-        mix_vec(h, hp, x, r[4], y);
+        for (int j = 0; j < 5; ++j) r[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (in) {
+            const uint4* slot = ring.next();
+#pragma unroll
+            for (int j = 0; j < 5; ++j) r[j] = slot[j * kThreads];
+        }
+        __syncwarp();
         int S[5];
 #pragma unroll
         for (int j = 0; j < 5; ++j) S[j] = mx_scale_byte<kFmt>(mx_block_max(mx_amax8(r[j])));
         if (in) {
+            const uint4 x[4] = {r[0], r[1], r[2], r[3]};
+            uint4 y[4];
+            mix_vec(h, hp, x, r[4], y);
 #pragma unroll
             for (int i = 0; i < 4; ++i) __stcs(Yt + (int64_t)i * CV + v, y[i]);
 #pragma unroll
@@ -136,24 +149,32 @@ __global__ void __launch_bounds__(kThreads)
 mix_fwd_ckpt_kernel(const uint4* X, const float* H, const float* hpost, const uint4* F, uint4* Y, CkptOut o,
                     int64_t T, int CV)
 {
-    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+    extern __shared__ uint4 ring_smem[];
+    FwdRing ring(ring_smem, X, nullptr, F, T, CV);
+    for (int64_t k = 0; k < ring.tokens(); ++k) {
+        const int64_t t = (int64_t)blockIdx.x + k * gridDim.x;
         float h[16], hp[4];
         load_maps(H, hpost, t, h, hp);
-        mix_token_fwd_ckpt<kFmt>(h, hp, X, F, Y, o, t, CV);
+        mix_token_fwd_ckpt<kFmt>(h, hp, ring, Y, o, t, CV);
     }
+    ring.drain();
 }
 
-// Fused projection + mix with the checkpoint: proj_mix_fwd_kernel of
-// mhc_mix.cu with the checkpoint written in the same pass.
+// Fused projection + mix with the checkpoint: the CTA's next kFusedTok tokens
+// are projected together, one thread each, as in proj_mix_fwd_kernel of
+// mhc_mix.cu, and then mixed one after the other in the ring's order.
 template <int kFmt>
 __global__ void __launch_bounds__(kThreads)
 proj_mix_fwd_ckpt_kernel(const float* logits, const float* hpost, const uint4* X, const uint4* F, uint4* Y,
                          float* Hout, CkptOut o, int64_t T, int CV, int maxit)
 {
+    extern __shared__ uint4 ring_smem[];
     __shared__ float sH[kFusedTok][16];
-    for (int64_t t0 = (int64_t)blockIdx.x * kFusedTok; t0 < T; t0 += (int64_t)gridDim.x * kFusedTok) {
-        if (threadIdx.x < kFusedTok && t0 + threadIdx.x < T) {
-            const int64_t t = t0 + threadIdx.x;
+    FwdRing ring(ring_smem, X, nullptr, F, T, CV);
+    const int64_t n = ring.tokens();
+    for (int64_t k0 = 0; k0 < n; k0 += kFusedTok) {
+        if (threadIdx.x < kFusedTok && k0 + threadIdx.x < n) {
+            const int64_t t = (int64_t)blockIdx.x + (k0 + threadIdx.x) * gridDim.x;
             float a[16];
             load16(logits + 16 * t, a);
             newton_project(a, maxit);
@@ -162,19 +183,21 @@ proj_mix_fwd_ckpt_kernel(const float* logits, const float* hpost, const uint4* X
             for (int k = 0; k < 16; ++k) sH[threadIdx.x][k] = a[k];
         }
         __syncthreads();
-        for (int k = 0; k < kFusedTok && t0 + k < T; ++k) {
+        for (int k = 0; k < kFusedTok && k0 + k < n; ++k) {
+            const int64_t t = (int64_t)blockIdx.x + (k0 + k) * gridDim.x;
             float h[16], hp[4];
 #pragma unroll
             for (int q = 0; q < 16; ++q) h[q] = sH[k][q];
-            const float4 hq = __ldg(reinterpret_cast<const float4*>(hpost) + t0 + k);
+            const float4 hq = __ldg(reinterpret_cast<const float4*>(hpost) + t);
             hp[0] = hq.x;
             hp[1] = hq.y;
             hp[2] = hq.z;
             hp[3] = hq.w;
-            mix_token_fwd_ckpt<kFmt>(h, hp, X, F, Y, o, t0 + k, CV);
+            mix_token_fwd_ckpt<kFmt>(h, hp, ring, Y, o, t, CV);
         }
         __syncthreads();
     }
+    ring.drain();
 }
 
 // ------------------------------------------------ backward from a checkpoint
@@ -528,9 +551,11 @@ cudaError_t launch_mix_fwd_ckpt(const uint16_t* X, const float* H, const float* 
                                 cudaStream_t s)
 {
     const auto kernel = format == MHC_MX_INT8 ? mix_fwd_ckpt_kernel<MHC_MX_INT8> : mix_fwd_ckpt_kernel<MHC_MX_E4M3>;
-    const int grid = persistent_grid((const void*)kernel, kThreads, 0, T);
-    kernel<<<grid, kThreads, 0, s>>>((const uint4*)X, H, hpost, (const uint4*)F, (uint4*)Y, CkptOut{Xc, Xs, Fc, Fs}, T,
-                                     (int)(C / 8));
+    constexpr int smem = FwdRing::kSmemBytes;
+    static_assert(smem <= 48 * 1024, "ring needs an opt-in");
+    const int grid = persistent_grid((const void*)kernel, kThreads, smem, T);
+    kernel<<<grid, kThreads, smem, s>>>((const uint4*)X, H, hpost, (const uint4*)F, (uint4*)Y,
+                                        CkptOut{Xc, Xs, Fc, Fs}, T, (int)(C / 8));
     return cudaGetLastError();
 }
 
@@ -540,9 +565,11 @@ cudaError_t launch_proj_mix_fwd_ckpt(const float* logits, const float* hpost, co
 {
     const auto kernel =
         format == MHC_MX_INT8 ? proj_mix_fwd_ckpt_kernel<MHC_MX_INT8> : proj_mix_fwd_ckpt_kernel<MHC_MX_E4M3>;
-    const int grid = persistent_grid((const void*)kernel, kThreads, 0, (T + kFusedTok - 1) / kFusedTok);
-    kernel<<<grid, kThreads, 0, s>>>(logits, hpost, (const uint4*)X, (const uint4*)F, (uint4*)Y, H,
-                                     CkptOut{Xc, Xs, Fc, Fs}, T, (int)(C / 8), maxit);
+    constexpr int smem = FwdRing::kSmemBytes;
+    static_assert(smem + kFusedTok * 64 <= 48 * 1024, "ring needs an opt-in");
+    const int grid = persistent_grid((const void*)kernel, kThreads, smem, (T + kFusedTok - 1) / kFusedTok);
+    kernel<<<grid, kThreads, smem, s>>>(logits, hpost, (const uint4*)X, (const uint4*)F, (uint4*)Y, H,
+                                        CkptOut{Xc, Xs, Fc, Fs}, T, (int)(C / 8), maxit);
     return cudaGetLastError();
 }
 
