@@ -31,61 +31,123 @@ constexpr int kFusedTok = 4;  // tokens projected together per CTA round
 
 // ------------------------------------------------------------ pack, restore
 
-// kPackThreads / lanes rows at a time: `lanes` (a power of two, 4..256) threads
-// walk one row, so that narrow rows share a CTA.
+// All rows' blocks in one sequence: four lanes hold a block, a CTA 64 of them
+// side by side, whatever the row length, and a thread goes on by the whole
+// grid's stride.  It keeps kPackAhead blocks in flight, and finds its row by
+// one division at the start and additions after it.
 constexpr int kPackThreads = 256;
+constexpr int kPackBlocks = kPackThreads / 4;
+constexpr int kPackAhead = 4;
+
+struct BlockWalk {
+    int64_t r, R, dr;              // row, rows, rows a stride
+    int64_t vec, dvec, sc, dsc;    // vector of 8 channels, scale byte: places from the first row's start
+    int k, NB, dk;                 // block in its row, blocks of a row, blocks a stride
+    int vec_wrap, sc_wrap, lanes;  // from past a row's last block to the next row's first; lanes of the last block
+
+    __device__ __forceinline__ BlockWalk(int64_t rows, int CV) : R(rows), NB((CV + 3) >> 2)
+    {
+        const int64_t first = (int64_t)blockIdx.x * kPackBlocks + (threadIdx.x >> 2);
+        const int64_t stride = (int64_t)gridDim.x * kPackBlocks;
+        const int sp = (int)mx_scale_pitch((int64_t)CV * 8);
+        r = first / NB;
+        k = (int)(first - r * NB);
+        dr = stride / NB;
+        dk = (int)(stride - dr * NB);
+        vec = r * CV + 4 * k + (threadIdx.x & 3);
+        dvec = dr * CV + 4 * dk;
+        sc = r * sp + k;
+        dsc = dr * sp + dk;
+        vec_wrap = CV - 4 * NB;
+        sc_wrap = sp - NB;
+        lanes = CV - 4 * (NB - 1);
+    }
+    __device__ __forceinline__ bool done() const { return r >= R; }
+    // whether this lane has a vector of the block
+    __device__ __forceinline__ bool in() const { return r < R && (k < NB - 1 || (int)(threadIdx.x & 3) < lanes); }
+    __device__ __forceinline__ void next()
+    {
+        r += dr;
+        k += dk;
+        vec += dvec;
+        sc += dsc;
+        if (k >= NB) {
+            k -= NB;
+            ++r;
+            vec += vec_wrap;
+            sc += sc_wrap;
+        }
+    }
+};
 
 template <int kFmt>
-__device__ __forceinline__ void store_codes(uint8_t* row, int v, const uint2 w)
+__device__ __forceinline__ void store_codes(uint8_t* codes, int64_t vec, const uint2 w)
 {
     if (kFmt == MHC_MX_E2M1)
-        __stcs(reinterpret_cast<uint32_t*>(row) + v, w.x);
+        __stcs(reinterpret_cast<uint32_t*>(codes) + vec, w.x);
     else
-        __stcs(reinterpret_cast<uint2*>(row) + v, w);
+        __stcs(reinterpret_cast<uint2*>(codes) + vec, w);
 }
 
 template <int kFmt>
-__device__ __forceinline__ uint2 load_codes(const uint8_t* row, int v)
+__device__ __forceinline__ uint2 load_codes(const uint8_t* codes, int64_t vec)
 {
-    if (kFmt == MHC_MX_E2M1) return make_uint2(__ldcs(reinterpret_cast<const uint32_t*>(row) + v), 0u);
-    return __ldcs(reinterpret_cast<const uint2*>(row) + v);
+    if (kFmt == MHC_MX_E2M1) return make_uint2(__ldcs(reinterpret_cast<const uint32_t*>(codes) + vec), 0u);
+    return __ldcs(reinterpret_cast<const uint2*>(codes) + vec);
 }
 
 template <int kFmt>
 __global__ void __launch_bounds__(kPackThreads)
-mx_pack_kernel(const uint4* x, uint8_t* codes, uint8_t* scales, int64_t R, int CV, int lanes)
+mx_pack_kernel(const uint4* x, uint8_t* codes, uint8_t* scales, int64_t R, int CV)
 {
-    const int rows = kPackThreads / lanes, lane = threadIdx.x & (lanes - 1);
-    const int64_t cp = mx_code_pitch(kFmt, (int64_t)CV * 8), sp = mx_scale_pitch((int64_t)CV * 8);
-    // the loops' bounds depend on the warp only: every lane takes part in the shuffles
-    for (int64_t r0 = (int64_t)blockIdx.x * rows; r0 < R; r0 += (int64_t)gridDim.x * rows) {
-        const int64_t r = r0 + threadIdx.x / lanes;
-        for (int v0 = 0; v0 < CV; v0 += lanes) {
-            const int v = v0 + lane;
-            const bool in = r < R && v < CV;
-            const uint4 q = in ? __ldcs(x + r * CV + v) : make_uint4(0u, 0u, 0u, 0u);
-            const int S = mx_scale_byte<kFmt>(mx_block_max(mx_amax8(q)));
+    BlockWalk w(R, CV);
+    // a warp goes on while any of its lanes has blocks: all take part in the shuffles
+    while (__any_sync(0xffffffffu, !w.done())) {
+        uint4 q[kPackAhead];
+        BlockWalk at = w;
+#pragma unroll
+        for (int u = 0; u < kPackAhead; ++u) {
+            q[u] = w.in() ? __ldcs(x + w.vec) : make_uint4(0u, 0u, 0u, 0u);
+            w.next();
+        }
+#pragma unroll
+        for (int u = 0; u < kPackAhead; ++u) {
+            const int S = mx_scale_byte<kFmt>(mx_block_max(mx_amax8(q[u])));
             float f[8];
-            unpack8(q, f);
-            if (in) {
-                store_codes<kFmt>(codes + r * cp, v, mx_encode8<kFmt>(f, S));
-                mx_store_scale(scales + r * sp, v, CV, S);
+            unpack8(q[u], f);
+            if (at.in()) {
+                store_codes<kFmt>(codes, at.vec, mx_encode8<kFmt>(f, S));
+                if ((threadIdx.x & 3) == 0) mx_store_scale(scales + at.sc, at.k, at.NB, S);
             }
+            at.next();
         }
     }
 }
 
 template <int kFmt>
 __global__ void __launch_bounds__(kPackThreads)
-mx_unpack_kernel(const uint8_t* codes, const uint8_t* scales, uint4* x, int64_t R, int CV, int lanes)
+mx_unpack_kernel(const uint8_t* codes, const uint8_t* scales, uint4* x, int64_t R, int CV)
 {
-    const int rows = kPackThreads / lanes, lane = threadIdx.x & (lanes - 1);
-    const int64_t cp = mx_code_pitch(kFmt, (int64_t)CV * 8), sp = mx_scale_pitch((int64_t)CV * 8);
-    for (int64_t r = (int64_t)blockIdx.x * rows + threadIdx.x / lanes; r < R; r += (int64_t)gridDim.x * rows) {
-        for (int v = lane; v < CV; v += lanes) {
-            float f[8];
-            mx_decode8<kFmt>(load_codes<kFmt>(codes + r * cp, v), mx_scale_value(__ldg(scales + r * sp + (v >> 2))), f);
-            __stcs(x + r * CV + v, pack8(f));
+    for (BlockWalk w(R, CV); !w.done();) {
+        uint2 q[kPackAhead];
+        int S[kPackAhead];
+        BlockWalk at = w;
+#pragma unroll
+        for (int u = 0; u < kPackAhead; ++u) {
+            if (w.in()) {
+                q[u] = load_codes<kFmt>(codes, w.vec);
+                S[u] = __ldg(scales + w.sc);
+            }
+            w.next();
+        }
+#pragma unroll
+        for (int u = 0; u < kPackAhead; ++u) {
+            if (at.in()) {
+                float f[8];
+                mx_decode8<kFmt>(q[u], mx_scale_value(S[u]), f);
+                __stcs(x + at.vec, pack8(f));
+            }
+            at.next();
         }
     }
 }
@@ -109,7 +171,7 @@ template <int kFmt>
 __device__ __forceinline__ void mix_token_fwd_ckpt(const float (&h)[16], const float (&hp)[4], FwdRing& ring, uint4* Y,
                                                    const CkptOut& o, int64_t t, int CV)
 {
-    const int64_t C = (int64_t)CV * 8, sp = mx_scale_pitch(C);
+    const int64_t sp = mx_scale_pitch((int64_t)CV * 8);
     uint4* Yt = Y + t * 4 * CV;
     // the bound depends on the warp only: every lane takes part in the shuffles
     for (int v = threadIdx.x; (v & ~31) < CV; v += kThreads) {
@@ -137,8 +199,9 @@ __device__ __forceinline__ void mix_token_fwd_ckpt(const float (&h)[16], const f
                 float f[8];
                 unpack8(r[j], f);
                 const int64_t row = j < 4 ? t * 4 + j : t;
-                store_codes<kFmt>((j < 4 ? o.Xc : o.Fc) + row * C, v, mx_encode8<kFmt>(f, S[j]));
-                mx_store_scale((j < 4 ? o.Xs : o.Fs) + row * sp, v, CV, S[j]);
+                store_codes<kFmt>(j < 4 ? o.Xc : o.Fc, row * CV + v, mx_encode8<kFmt>(f, S[j]));
+                if ((v & 3) == 0)
+                    mx_store_scale((j < 4 ? o.Xs : o.Fs) + row * sp + (v >> 2), v >> 2, (CV + 3) >> 2, S[j]);
             }
         }
     }
@@ -403,7 +466,7 @@ mix_post_bwd_ckpt_kernel(const uint4* dY, const uint8_t* Fc, const uint8_t* Fs, 
 {
     __shared__ float red[kWarps * 4];
     __shared__ float tot[4];
-    const int64_t C = (int64_t)CV * 8, sp = mx_scale_pitch(C);
+    const int64_t sp = mx_scale_pitch((int64_t)CV * 8);
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         const float4 q = __ldg(reinterpret_cast<const float4*>(hpost) + t);
         const float hp[4] = {q.x, q.y, q.z, q.w};
@@ -411,7 +474,7 @@ mix_post_bwd_ckpt_kernel(const uint4* dY, const uint8_t* Fc, const uint8_t* Fs, 
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int v = threadIdx.x; v < CV; v += kThreads) {
             float ff[8], o[8];
-            mx_decode8<kFmt>(load_codes<kFmt>(Fc + t * C, v), mx_scale_value(__ldg(Fs + t * sp + (v >> 2))), ff);
+            mx_decode8<kFmt>(load_codes<kFmt>(Fc, t * CV + v), mx_scale_value(__ldg(Fs + t * sp + (v >> 2))), ff);
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = 0.0f;
 #pragma unroll
@@ -499,30 +562,26 @@ mix_premap_bwd_ckpt_kernel(CkptIn in, const float* H, const float* hpre, const u
     ring.drain();
 }
 
-// Threads that walk one row: the power of two (4..256) that covers it, so
-// that rows of a few vectors share a CTA.
-int pack_lanes(int CV)
+// CTAs that cover all blocks of R rows, kPackAhead a thread.
+int64_t pack_ctas(int64_t R, int CV)
 {
-    int lanes = 4;
-    while (lanes < CV && lanes < kPackThreads) lanes *= 2;
-    return lanes;
+    const int64_t blocks = R * ((CV + 3) / 4);
+    return (blocks + kPackBlocks * kPackAhead - 1) / (kPackBlocks * kPackAhead);
 }
 
 template <int kFmt>
 cudaError_t pack(const uint16_t* x, uint8_t* codes, uint8_t* scales, int64_t R, int CV, cudaStream_t s)
 {
-    const int lanes = pack_lanes(CV), rows = kPackThreads / lanes;
-    const int grid = persistent_grid((const void*)mx_pack_kernel<kFmt>, kPackThreads, 0, (R + rows - 1) / rows);
-    mx_pack_kernel<kFmt><<<grid, kPackThreads, 0, s>>>((const uint4*)x, codes, scales, R, CV, lanes);
+    const int grid = persistent_grid((const void*)mx_pack_kernel<kFmt>, kPackThreads, 0, pack_ctas(R, CV));
+    mx_pack_kernel<kFmt><<<grid, kPackThreads, 0, s>>>((const uint4*)x, codes, scales, R, CV);
     return cudaGetLastError();
 }
 
 template <int kFmt>
 cudaError_t unpack(const uint8_t* codes, const uint8_t* scales, uint16_t* x, int64_t R, int CV, cudaStream_t s)
 {
-    const int lanes = pack_lanes(CV), rows = kPackThreads / lanes;
-    const int grid = persistent_grid((const void*)mx_unpack_kernel<kFmt>, kPackThreads, 0, (R + rows - 1) / rows);
-    mx_unpack_kernel<kFmt><<<grid, kPackThreads, 0, s>>>(codes, scales, (uint4*)x, R, CV, lanes);
+    const int grid = persistent_grid((const void*)mx_unpack_kernel<kFmt>, kPackThreads, 0, pack_ctas(R, CV));
+    mx_unpack_kernel<kFmt><<<grid, kPackThreads, 0, s>>>(codes, scales, (uint4*)x, R, CV);
     return cudaGetLastError();
 }
 

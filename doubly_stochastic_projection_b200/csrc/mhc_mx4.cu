@@ -53,7 +53,7 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
         const int S = mx_scale_byte<MHC_MX_E2M1>(mx_block_max(mx_amax8(o)));
         if (in) {
             reinterpret_cast<uint32_t*>(codes)[t * CV + v] = mx_encode8<MHC_MX_E2M1>(o, S).x;
-            mx_store_scale(scales + t * sp, v, CV, S);
+            if ((v & 3) == 0) mx_store_scale(scales + t * sp + (v >> 2), v >> 2, (CV + 3) >> 2, S);
         }
     }
 }

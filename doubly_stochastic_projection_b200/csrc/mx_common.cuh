@@ -90,23 +90,31 @@ __device__ __forceinline__ float mx_inverse_scale(int S)
 template <int kFmt>
 __device__ __forceinline__ uint2 mx_encode8(const float (&f)[8], int S)
 {
+    if constexpr (kFmt == MHC_MX_INT8) {
+        // fma with 1.5 * 2^23 rounds 64 q to an integer, ties to even, into the
+        // low bits.  64 / scale is a float for S >= 6, and |64 q| passes 127 at
+        // S = 254 only; the other scales take the long way
+        uint32_t b[8];
+        if (S >= 6 && S < 254) {
+            const float inv64 = __uint_as_float((uint32_t)(260 - S) << 23);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] = __float_as_uint(fmaf(f[e], inv64, 12582912.0f));
+        } else {
+            if (S == kMxScaleNaN) return make_uint2(0u, 0u);
+            const float inv = mx_inverse_scale(S);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                b[e] = __float_as_uint(fmaf(fminf(fmaxf(f[e] * inv, -1.984375f), 1.984375f), 64.0f, 12582912.0f));
+        }
+        return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                          __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+    }
     if (S == kMxScaleNaN) return make_uint2(0u, 0u);
     const float inv = mx_inverse_scale(S);
     float q[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) q[e] = f[e] * inv;
-    if constexpr (kFmt == MHC_MX_INT8) {
-        uint32_t b[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            // the sum with 1.5 * 2^23 rounds 64 q to an integer, ties to even,
-            // into the low bits; only S = 254 can leave |64 q| above 127
-            if (S == 254) q[e] = fminf(fmaxf(q[e], -1.984375f), 1.984375f);
-            b[e] = __float_as_uint(fmaf(q[e], 64.0f, 12582912.0f));
-        }
-        return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
-                          __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
-    } else if constexpr (kFmt == MHC_MX_E4M3) {
+    if constexpr (kFmt == MHC_MX_E4M3) {
         uint16_t p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -192,16 +200,13 @@ __device__ __forceinline__ uint32_t mx_amax8(const float (&f)[8])
     return m;
 }
 
-// Writes the scale byte of vector v's block (every block's first lane), and the
-// row's padding with its last block.
-__device__ __forceinline__ void mx_store_scale(uint8_t* row, int v, int CV, int S)
+// Writes the scale byte of block k of NB, at its place, and the row's padding
+// with its last block.
+__device__ __forceinline__ void mx_store_scale(uint8_t* at, int k, int NB, int S)
 {
-    if ((v & 3) == 0 && v < CV) {
-        const int b = v >> 2, blocks = (CV + 3) >> 2;
-        row[b] = (uint8_t)S;
-        if (b == blocks - 1)
-            for (int p = blocks; p & 3; ++p) row[p] = 0;
-    }
+    at[0] = (uint8_t)S;
+    if (k == NB - 1)
+        for (int p = 1; (k + p) & 3; ++p) at[p] = 0;
 }
 
 }  // namespace mhc
