@@ -31,40 +31,43 @@ constexpr int kFusedTok = 4;  // tokens projected together per CTA round
 
 // ------------------------------------------------------------ pack, restore
 
-// All rows' blocks in one sequence: four lanes hold a block, a CTA 64 of them
-// side by side, whatever the row length, and a thread goes on by the whole
-// grid's stride.  It keeps kPackAhead blocks in flight, and finds its row by
-// one division at the start and additions after it.
+// All rows' blocks in one sequence: two lanes hold a block, 16 channels each, a
+// CTA 128 blocks side by side, whatever the row length, and a thread goes on
+// by the whole grid's stride.  It keeps kPackAhead pieces in flight, and finds
+// its row by one division at the start and additions after it.  With 8
+// channels a lane the pack was bound by its instructions (118 for 32 vectors,
+// 69% of the issue slots, at 78% of the copy bandwidth).
 constexpr int kPackThreads = 256;
-constexpr int kPackBlocks = kPackThreads / 4;
-constexpr int kPackAhead = 4;
+constexpr int kPackBlocks = kPackThreads / 2;
+constexpr int kPackAhead = 2;
 
 struct BlockWalk {
-    int64_t r, R, dr;              // row, rows, rows a stride
-    int64_t vec, dvec, sc, dsc;    // vector of 8 channels, scale byte: places from the first row's start
-    int k, NB, dk;                 // block in its row, blocks of a row, blocks a stride
-    int vec_wrap, sc_wrap, lanes;  // from past a row's last block to the next row's first; lanes of the last block
+    int64_t r, R, dr;            // row, rows, rows a stride
+    int64_t vec, dvec, sc, dsc;  // vector of 8 channels, scale byte: places from the first row's start
+    int k, NB, dk;               // block in its row, blocks of a row, blocks a stride
+    int vec_wrap, sc_wrap;       // from past a row's last block to the next row's first
+    int last;                    // this lane's vectors in a row's last block: 2, 1 or none
 
     __device__ __forceinline__ BlockWalk(int64_t rows, int CV) : R(rows), NB((CV + 3) >> 2)
     {
-        const int64_t first = (int64_t)blockIdx.x * kPackBlocks + (threadIdx.x >> 2);
+        const int64_t first = (int64_t)blockIdx.x * kPackBlocks + (threadIdx.x >> 1);
         const int64_t stride = (int64_t)gridDim.x * kPackBlocks;
-        const int sp = (int)mx_scale_pitch((int64_t)CV * 8);
+        const int sp = (int)mx_scale_pitch((int64_t)CV * 8), off = 2 * (threadIdx.x & 1);
         r = first / NB;
         k = (int)(first - r * NB);
         dr = stride / NB;
         dk = (int)(stride - dr * NB);
-        vec = r * CV + 4 * k + (threadIdx.x & 3);
+        vec = r * CV + 4 * k + off;
         dvec = dr * CV + 4 * dk;
         sc = r * sp + k;
         dsc = dr * sp + dk;
         vec_wrap = CV - 4 * NB;
         sc_wrap = sp - NB;
-        lanes = CV - 4 * (NB - 1);
+        last = CV - 4 * (NB - 1) - off;
     }
     __device__ __forceinline__ bool done() const { return r >= R; }
-    // whether this lane has a vector of the block
-    __device__ __forceinline__ bool in() const { return r < R && (k < NB - 1 || (int)(threadIdx.x & 3) < lanes); }
+    // vectors that this lane has of the block: 2, 1, or 0 and less
+    __device__ __forceinline__ int count() const { return r >= R ? 0 : k < NB - 1 ? 2 : last; }
     __device__ __forceinline__ void next()
     {
         r += dr;
@@ -79,6 +82,38 @@ struct BlockWalk {
         }
     }
 };
+
+// Two vectors of 8 channels side by side.  kWide (rows of a multiple of 16
+// channels, x on a 32-byte boundary): 32 bytes of bf16, or 16 of 8-bit codes,
+// in one access; else vector by vector, of which `n` exist.  Pack of int8 at
+// 16384 x 8192: 64 us wide, 68 not; its restore 69 and 78.
+template <bool kWide>
+__device__ __forceinline__ void load_two(const uint4* p, int n, uint4 (&q)[2])
+{
+    q[0] = q[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (n <= 0) return;
+    if constexpr (kWide) {
+        asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w), "=r"(q[1].x), "=r"(q[1].y),
+                       "=r"(q[1].z), "=r"(q[1].w)
+                     : "l"(p));
+    } else {
+        q[0] = __ldcs(p);
+        if (n > 1) q[1] = __ldcs(p + 1);
+    }
+}
+template <bool kWide>
+__device__ __forceinline__ void store_two(uint4* p, int n, const uint4 (&q)[2])
+{
+    if constexpr (kWide) {
+        asm volatile("st.global.cs.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(q[0].x), "r"(q[0].y),
+                     "r"(q[0].z), "r"(q[0].w), "r"(q[1].x), "r"(q[1].y), "r"(q[1].z), "r"(q[1].w), "l"(p)
+                     : "memory");
+    } else {
+        __stcs(p, q[0]);
+        if (n > 1) __stcs(p + 1, q[1]);
+    }
+}
 
 template <int kFmt>
 __device__ __forceinline__ void store_codes(uint8_t* codes, int64_t vec, const uint2 w)
@@ -96,56 +131,96 @@ __device__ __forceinline__ uint2 load_codes(const uint8_t* codes, int64_t vec)
     return __ldcs(reinterpret_cast<const uint2*>(codes) + vec);
 }
 
-template <int kFmt>
+template <int kFmt, bool kWide>
+__device__ __forceinline__ void store_two_codes(uint8_t* codes, int64_t vec, int n, const uint2 (&w)[2])
+{
+    if (!kWide) {
+        store_codes<kFmt>(codes, vec, w[0]);
+        if (n > 1) store_codes<kFmt>(codes, vec + 1, w[1]);
+    } else if (kFmt == MHC_MX_E2M1) {
+        __stcs(reinterpret_cast<uint2*>(codes + 4 * vec), make_uint2(w[0].x, w[1].x));
+    } else {
+        __stcs(reinterpret_cast<uint4*>(codes + 8 * vec), make_uint4(w[0].x, w[0].y, w[1].x, w[1].y));
+    }
+}
+template <int kFmt, bool kWide>
+__device__ __forceinline__ void load_two_codes(const uint8_t* codes, int64_t vec, int n, uint2 (&w)[2])
+{
+    w[0] = w[1] = make_uint2(0u, 0u);
+    if (n <= 0) return;
+    if (!kWide) {
+        w[0] = load_codes<kFmt>(codes, vec);
+        if (n > 1) w[1] = load_codes<kFmt>(codes, vec + 1);
+    } else if (kFmt == MHC_MX_E2M1) {
+        const uint2 q = __ldcs(reinterpret_cast<const uint2*>(codes + 4 * vec));
+        w[0].x = q.x, w[1].x = q.y;
+    } else {
+        const uint4 q = __ldcs(reinterpret_cast<const uint4*>(codes + 8 * vec));
+        w[0] = make_uint2(q.x, q.y), w[1] = make_uint2(q.z, q.w);
+    }
+}
+
+template <int kFmt, bool kWide>
 __global__ void __launch_bounds__(kPackThreads)
 mx_pack_kernel(const uint4* x, uint8_t* codes, uint8_t* scales, int64_t R, int CV)
 {
     BlockWalk w(R, CV);
     // a warp goes on while any of its lanes has blocks: all take part in the shuffles
     while (__any_sync(0xffffffffu, !w.done())) {
-        uint4 q[kPackAhead];
+        uint4 q[kPackAhead][2];
         BlockWalk at = w;
 #pragma unroll
         for (int u = 0; u < kPackAhead; ++u) {
-            q[u] = w.in() ? __ldcs(x + w.vec) : make_uint4(0u, 0u, 0u, 0u);
+            load_two<kWide>(x + w.vec, w.count(), q[u]);
             w.next();
         }
 #pragma unroll
         for (int u = 0; u < kPackAhead; ++u) {
-            const int S = mx_scale_byte<kFmt>(mx_block_max(mx_amax8(q[u])));
-            float f[8];
-            unpack8(q[u], f);
-            if (at.in()) {
-                store_codes<kFmt>(codes, at.vec, mx_encode8<kFmt>(f, S));
-                if ((threadIdx.x & 3) == 0) mx_store_scale(scales + at.sc, at.k, at.NB, S);
+            const uint32_t m = max(mx_amax8(q[u][0]), mx_amax8(q[u][1]));
+            const int S = mx_scale_byte<kFmt>(max(m, __shfl_xor_sync(0xffffffffu, m, 1)));
+            const int n = at.count();
+            if (n > 0) {
+                uint2 c[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float f[8];
+                    unpack8(q[u][i], f);
+                    c[i] = mx_encode8<kFmt>(f, S);
+                }
+                store_two_codes<kFmt, kWide>(codes, at.vec, n, c);
+                if ((threadIdx.x & 1) == 0) mx_store_scale(scales + at.sc, at.k, at.NB, S);
             }
             at.next();
         }
     }
 }
 
-template <int kFmt>
+template <int kFmt, bool kWide>
 __global__ void __launch_bounds__(kPackThreads)
 mx_unpack_kernel(const uint8_t* codes, const uint8_t* scales, uint4* x, int64_t R, int CV)
 {
     for (BlockWalk w(R, CV); !w.done();) {
-        uint2 q[kPackAhead];
+        uint2 c[kPackAhead][2];
         int S[kPackAhead];
         BlockWalk at = w;
 #pragma unroll
         for (int u = 0; u < kPackAhead; ++u) {
-            if (w.in()) {
-                q[u] = load_codes<kFmt>(codes, w.vec);
-                S[u] = __ldg(scales + w.sc);
-            }
+            load_two_codes<kFmt, kWide>(codes, w.vec, w.count(), c[u]);
+            if (!w.done()) S[u] = __ldg(scales + w.sc);
             w.next();
         }
 #pragma unroll
         for (int u = 0; u < kPackAhead; ++u) {
-            if (at.in()) {
-                float f[8];
-                mx_decode8<kFmt>(q[u], mx_scale_value(S[u]), f);
-                __stcs(x + at.vec, pack8(f));
+            const int n = at.count();
+            if (n > 0) {
+                uint4 q[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float f[8];
+                    mx_decode8<kFmt>(c[u][i], mx_scale_value(S[u]), f);
+                    q[i] = pack8(f);
+                }
+                store_two<kWide>(x + at.vec, n, q);
             }
             at.next();
         }
@@ -569,19 +644,23 @@ int64_t pack_ctas(int64_t R, int CV)
     return (blocks + kPackBlocks * kPackAhead - 1) / (kPackBlocks * kPackAhead);
 }
 
+bool wide_rows(const uint16_t* x, int CV) { return CV % 2 == 0 && (reinterpret_cast<uintptr_t>(x) & 31) == 0; }
+
 template <int kFmt>
 cudaError_t pack(const uint16_t* x, uint8_t* codes, uint8_t* scales, int64_t R, int CV, cudaStream_t s)
 {
-    const int grid = persistent_grid((const void*)mx_pack_kernel<kFmt>, kPackThreads, 0, pack_ctas(R, CV));
-    mx_pack_kernel<kFmt><<<grid, kPackThreads, 0, s>>>((const uint4*)x, codes, scales, R, CV);
+    const auto kernel = wide_rows(x, CV) ? mx_pack_kernel<kFmt, true> : mx_pack_kernel<kFmt, false>;
+    const int grid = persistent_grid((const void*)kernel, kPackThreads, 0, pack_ctas(R, CV));
+    kernel<<<grid, kPackThreads, 0, s>>>((const uint4*)x, codes, scales, R, CV);
     return cudaGetLastError();
 }
 
 template <int kFmt>
 cudaError_t unpack(const uint8_t* codes, const uint8_t* scales, uint16_t* x, int64_t R, int CV, cudaStream_t s)
 {
-    const int grid = persistent_grid((const void*)mx_unpack_kernel<kFmt>, kPackThreads, 0, pack_ctas(R, CV));
-    mx_unpack_kernel<kFmt><<<grid, kPackThreads, 0, s>>>(codes, scales, (uint4*)x, R, CV);
+    const auto kernel = wide_rows(x, CV) ? mx_unpack_kernel<kFmt, true> : mx_unpack_kernel<kFmt, false>;
+    const int grid = persistent_grid((const void*)kernel, kPackThreads, 0, pack_ctas(R, CV));
+    kernel<<<grid, kPackThreads, 0, s>>>(codes, scales, (uint4*)x, R, CV);
     return cudaGetLastError();
 }
 

@@ -66,6 +66,22 @@ def as_bf16(v64):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("C", [64, 72])
+def test_rows_on_sixteen_byte_boundaries_only(fmt, C):
+    # the alignment that is asked for is 16 bytes: rows that start between two
+    # 32-byte boundaries, in and out
+    flat = streams((1, 8 + 20 * C), 7)[0]
+    x = flat[8:].view(20, C)
+    assert x.data_ptr() % 32 == 16
+    q = api.mx_pack(x, fmt)
+    assert_codes(q, to_np64(x), fmt)
+    out = torch.full((16 + 20 * C,), 7.0, dtype=torch.bfloat16, device=dev())
+    y = api.mx_unpack(q, out=out[8:8 + 20 * C].view(20, C))
+    assert torch.equal(y, api.mx_unpack(q))
+    assert (out[:8] == 7).all() and (out[8 + 20 * C:] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_every_code_restores(fmt):
     codes = np.arange(256, dtype=np.uint8)[None].repeat(256, 0)  # row r: every code at scale r
     C = 512 if fmt == "e2m1" else 256
