@@ -82,7 +82,6 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 // NaN in the outputs that are not done.
 
 constexpr int kChan = 128;      // channels of a tile
-constexpr int kStepBytes = 128; // bytes of K of a tile: 256 elements
 constexpr int kProdThreads = 416;  // 13 warps, four on one scheduler: 128 registers a thread at most
 constexpr int kEpiWarps = 8;
 constexpr int kEpiThreads = 32 * kEpiWarps;
@@ -101,23 +100,26 @@ struct ProductArgs {
     int chan_tiles, tok_tiles;
 };
 
-template <int kTok_, int kStages_, bool kSplit_>
+template <int kTok_, int kRowBytes_, int kStages_, bool kSplit_>
 struct ProductShape {
     static constexpr int kTok = kTok_, kStages = kStages_;
+    static constexpr int kRowBytes = kRowBytes_;  // bytes of K of a tile: twice as many elements
     static constexpr bool kSplit = kSplit_;
     static constexpr int kTokChunks = (kTok + 127) / 128;  // 128-row chunks of A's scales
-    static constexpr int kWBytes = kChan * kStepBytes, kABytes = kTok * kStepBytes;
+    static constexpr int kWBytes = kChan * kRowBytes, kABytes = kTok * kRowBytes;
     static constexpr int kStageBytes = kWBytes + kABytes;
-    // scales: two buffers of four K tiles, a tile's being two halves (of 128
-    // elements) of one chunk of W's and kTokChunks of A's
-    static constexpr int kScaleTile = 2 * 512 * (1 + kTokChunks), kScaleBytes = 2 * 4 * kScaleTile;
+    // scales: two buffers of eight steps of 128 elements, a step's being one
+    // chunk of W's and kTokChunks of A's
+    static constexpr int kSteps = kRowBytes / 64;  // steps of 128 elements in a K tile
+    static constexpr int kBufTiles = 8 / kSteps;
+    static constexpr int kScaleStep = 512 * (1 + kTokChunks), kScaleBytes = 2 * 8 * kScaleStep;
     static constexpr int kSums = kSplit ? 1 : 2;  // accumulator tiles
     // the epilogue's: two buffers of 32 tokens, or the whole tile's partial sums
     static constexpr int kEpiBytes = (kSplit ? kTok : 64) * kChan * 4;
     static constexpr int kBars = 2 * kStages + 4 + 2 * kSums + 1;
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kScaleBytes + kEpiBytes + 8 * kBars + 16;
     // columns of tensor memory: sums, then each stage's scales of W and A
-    static constexpr int kScaleCols = 8 + 8 * kTokChunks;
+    static constexpr int kScaleCols = kSteps * 4 * (1 + kTokChunks);
     static constexpr int kSumCols = (kSums * kTok + 31) / 32 * 32;
     static constexpr int kColumns = 512;
     static_assert(kSumCols + kStages * kScaleCols <= kColumns, "tensor memory");
@@ -127,28 +129,38 @@ struct ProductShape {
     static_assert(kSmemBytes > 116 * 1024 && kSmemBytes <= 227 * 1024, "shared memory");
 };
 
-// The scales of a pair of K tiles (512 elements) of one row: 16 bytes, fetched
-// at once where rows start on 16 bytes (wide) and word by word where not
-// (words past the row read as zero).  Volatile, so that the loads stay where
-// they are issued, a round ahead of their use.
-__device__ __forceinline__ uint4 fetch_scales(const uint8_t* row, int pair, int pitch, bool wide)
+// The scales of 512 elements of one row, and of the next 512 if `two`: 16 bytes
+// each, in as few loads as the rows' alignment (32, 16 or 4 bytes) allows,
+// since every lane reads another row and each load costs a pass over 32 cache
+// lines.  Words past the row read as zero.  Volatile, so that the loads stay
+// where they are issued, a round ahead of their use.
+__device__ __forceinline__ void fetch_scales(const uint8_t* row, int pair, bool two, int pitch, int align, uint4& q0,
+                                             uint4& q1)
 {
-    uint4 q;
-    if (wide) {
-        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                     : "l"(row + 16 * pair));
+    const uint8_t* at = row + 16 * pair;
+    if (align == 32 && two) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(q0.x), "=r"(q0.y), "=r"(q0.z), "=r"(q0.w), "=r"(q1.x), "=r"(q1.y), "=r"(q1.z), "=r"(q1.w)
+                     : "l"(at));
+    } else if (align >= 16) {
+        asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q0.x), "=r"(q0.y), "=r"(q0.z), "=r"(q0.w)
+                     : "l"(at));
+        if (two)
+            asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(q1.x), "=r"(q1.y), "=r"(q1.z), "=r"(q1.w)
+                         : "l"(at + 16));
     } else {
-        uint32_t w[4];
+        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int at = 16 * pair + 4 * j;
+        for (int j = 0; j < 8; ++j) {
             w[j] = 0u;
-            if (at < pitch) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(w[j]) : "l"(row + at));
+            if (16 * pair + 4 * j < pitch && (j < 4 || two))
+                asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(w[j]) : "l"(at + 4 * j));
         }
-        q = make_uint4(w[0], w[1], w[2], w[3]);
+        q0 = make_uint4(w[0], w[1], w[2], w[3]);
+        q1 = make_uint4(w[4], w[5], w[6], w[7]);
     }
-    return q;
 }
 
 // Word w of a row's scales without the bytes past its KB blocks: what lies
@@ -244,9 +256,11 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
 
     // this CTA's output tiles, and its share of K in pairs of tiles
     const int ranks = S::kSplit ? (int)tc5::cluster_size() : 1, rank = S::kSplit ? (int)tc5::cluster_rank() : 0;
-    const int ktiles = (p.K / 2 + kStepBytes - 1) / kStepBytes, pairs = (ktiles + 1) / 2;
+    const int pairs = (p.K + 511) / 512;  // 16 bytes of scales
     const int pair0 = pairs * rank / ranks, pair1 = pairs * (rank + 1) / ranks;
-    const int k0 = 2 * pair0, k1 = min(2 * pair1, ktiles);
+    constexpr int kPairTiles = 256 / S::kRowBytes;
+    const int ktiles = (p.K / 2 + S::kRowBytes - 1) / S::kRowBytes;
+    const int k0 = kPairTiles * pair0, k1 = min(kPairTiles * pair1, ktiles);
     const int tiles = p.chan_tiles * p.tok_tiles;
     const int first = blockIdx.x / ranks, stride = gridDim.x / ranks;
     bool ok = true;
@@ -263,8 +277,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 const uint32_t at = base + s * S::kStageBytes;
                 if (tc5::elect_one()) {
                     tc5::mbar_expect_tx(full(s), S::kWBytes + S::kABytes);
-                    tc5::tma_load_2d(at, &mapW, k * kStepBytes, n0, full(s));
-                    tc5::tma_load_2d(at + kOffA, &mapA, k * kStepBytes, t0, full(s));
+                    tc5::tma_load_2d(at, &mapW, k * S::kRowBytes, n0, full(s));
+                    tc5::tma_load_2d(at + kOffA, &mapA, k * S::kRowBytes, t0, full(s));
                 }
                 __syncwarp();
                 s = s + 1 == kStages ? 0 : s + 1;
@@ -282,15 +296,16 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         uint32_t phase = 0, par = 0;
         for (int n = 0; n < mine && ok; ++n) {
             for (int k = 0; k < steps; ++k) {
-                if ((k & 3) == 0 && !(ok = tc5::mbar_wait_warp(scales_full(buf), par, abort))) break;
+                const int j = k & (S::kBufTiles - 1);  // in this buffer
+                if (j == 0 && !(ok = tc5::mbar_wait_warp(scales_full(buf), par, abort))) break;
                 if (!(ok = tc5::mbar_wait_warp(empty(s), phase ^ 1, abort))) break;
                 tc5::fence_after_sync();
-                const uint32_t at = base + kOffScales + (buf * 4 + (k & 3)) * S::kScaleTile;
+                const uint32_t at = base + kOffScales + (buf * 8 + j * S::kSteps) * S::kScaleStep;
                 const uint32_t sw = tmem + S::kSumCols + s * S::kScaleCols;
-                const bool last = (k & 3) == 3 || k + 1 == steps;  // of this buffer
+                const bool last = j + 1 == S::kBufTiles || k + 1 == steps;
                 if (tc5::elect_one()) {
 #pragma unroll
-                    for (int c = 0; c < 2 * (1 + S::kTokChunks); ++c)
+                    for (int c = 0; c < S::kSteps * (1 + S::kTokChunks); ++c)
                         tc5::copy_scales(sw + 4 * c, tc5::scale_desc(at + 512 * c));
                     tc5::commit(full(s));
                     if (last) tc5::commit(scales_empty(buf));
@@ -323,13 +338,16 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 if (!(ok = tc5::mbar_wait_warp(full(s), phase, abort))) break;
                 tc5::fence_after_sync();
                 const uint32_t at = base + s * S::kStageBytes;
-                const uint32_t sw = tmem + S::kSumCols + s * S::kScaleCols, sa = sw + 8;
-                const uint64_t dw = tc5::operand_desc(at), da = tc5::operand_desc(at + kOffA);
+                const uint32_t sc = tmem + S::kSumCols + s * S::kScaleCols;
+                const uint64_t dw = tc5::operand_desc<S::kRowBytes>(at);
+                const uint64_t da = tc5::operand_desc<S::kRowBytes>(at + kOffA);
                 if (tc5::elect_one()) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)  // 64 elements: 32 bytes along the swizzled row
-                        tc5::mma_mx4(d, dw + 2 * q, da + 2 * q, inst | tc5::scale_select(2 * (q & 1)), sw + 4 * (q >> 1),
-                                     sa + 4 * S::kTokChunks * (q >> 1), k > 0 || q > 0);
+                    for (int q = 0; q < 2 * S::kSteps; ++q) {  // 64 elements: 32 bytes along the swizzled row
+                        const uint32_t sw = sc + 4 * (1 + S::kTokChunks) * (q >> 1);
+                        tc5::mma_mx4(d, dw + 2 * q, da + 2 * q, inst | tc5::scale_select(2 * (q & 1)), sw, sw + 4,
+                                     k > 0 || q > 0);
+                    }
                     tc5::commit(empty(s));
                     if (k + 1 == steps) tc5::commit(sum_full(a));
                 }
@@ -349,7 +367,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         const bool isW = warp == 2;
         const uint8_t* src = isW ? p.Ws : p.As;
         const int KB = p.K / kMxBlock, pitch = (int)mx_scale_pitch(p.K);
-        const bool wide = (pitch & 15) == 0;
+        // of every pair of 512 elements that is fetched together
+        const int align = (pitch & 31) == 0 && (reinterpret_cast<uintptr_t>(src) & 31) == 0 && (pair0 & 1) == 0 ? 32
+                          : (pitch & 15) == 0                                                                ? 16
+                                                                                                             : 4;
         const int64_t rows = isW ? (int64_t)p.N : p.T;
         constexpr int kGroups = (kTok + 31) / 32 > 4 ? (kTok + 31) / 32 : 4;
         const int groups = isW ? 4 : (kTok + 31) / 32;
@@ -363,9 +384,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 if (g >= groups) break;
                 // rows past the end stand in for none: what they give is not written
                 const uint8_t* row = src + min(r0 + 32 * g + lane, rows - 1) * pitch;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    if (pair + u < pair1) next[u][g] = fetch_scales(row, pair + u, pitch, wide);
+                fetch_scales(row, pair, pair + 1 < pair1, pitch, align, next[0][g], next[1][g]);
             }
         };
         int buf = 0;
@@ -375,29 +394,26 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
             for (int pair = pair0; pair < pair1 && ok; pair += 2) {
                 if (!(ok = tc5::mbar_wait(scales_empty(buf), par ^ 1, abort))) break;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {  // K tiles
-                    const int k = 2 * pair + j;
-                    if (k >= k1) break;
-                    uint8_t* at = smem + kOffScales + (buf * 4 + j) * S::kScaleTile + (isW ? 0 : 1024);
+                for (int j = 0; j < 8; ++j) {  // steps of 128 elements, one word of scales a row
+                    const int w0 = 4 * pair + j;
+                    if (pair + j / 4 >= pair1) break;
+                    uint8_t* at = smem + kOffScales + (buf * 8 + j) * S::kScaleStep + (isW ? 0 : 512);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int c = 0; c < (kGroups + 3) / 4; ++c) {
+                        if (4 * c >= groups) break;
+                        uint32_t w[4];
 #pragma unroll
-                        for (int c = 0; c < (kGroups + 3) / 4; ++c) {
-                            if (4 * c >= groups) break;
-                            uint32_t w[4];
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const int r = 4 * c + g;
-                                w[g] = 0u;
-                                if (r < kGroups && r < groups) {
-                                    const uint4 q = next[j >> 1][r < kGroups ? r : 0];
-                                    w[g] = (j & 1) == 0 ? (h == 0 ? q.x : q.y) : (h == 0 ? q.z : q.w);
-                                }
-                                if (8 * (k + 1) > KB) w[g] = scales_within(w[g], 2 * k + h, KB);
+                        for (int g = 0; g < 4; ++g) {
+                            const int r = 4 * c + g;
+                            w[g] = 0u;
+                            if (r < kGroups && r < groups) {
+                                const uint4 q = next[j >> 2][r < kGroups ? r : 0];
+                                w[g] = (j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w;
                             }
-                            const int chunk = isW ? h : h * S::kTokChunks + c;
-                            reinterpret_cast<uint4*>(at + 512 * chunk)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+                            if (4 * (w0 + 1) > KB) w[g] = scales_within(w[g], w0, KB);
                         }
+                        reinterpret_cast<uint4*>(at + 512 * c)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 }
                 tc5::fence_async_shared();
                 __syncwarp();
@@ -513,7 +529,7 @@ cudaError_t launch_premap_fwd_mx4(const uint16_t* X, const float* hpre, uint8_t*
 
 namespace {
 
-// A byte matrix [rows][pitch] read in boxes of box_rows x 128 bytes.
+// A byte matrix [rows][pitch] read in boxes of box_rows x box_bytes (128 or 64).
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -535,13 +551,14 @@ EncodeTiled encode_tiled()
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-bool code_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box_rows)
+bool code_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box_rows, int box_bytes)
 {
     const EncodeTiled f = encode_tiled();
     const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(K / 2)};
-    const cuuint32_t box[2] = {kStepBytes, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows}, step[2] = {1, 1};
     return f != nullptr && f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box,
-                             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                             box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -563,9 +580,10 @@ cudaError_t product(const uint8_t* A, const uint8_t* W, ProductArgs p, cudaStrea
     const int64_t tiles = (int64_t)p.chan_tiles * p.tok_tiles;
     if (tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
     CUtensorMap mapW, mapA;
-    if (!code_map(&mapW, W, p.N, p.K, kChan) || !code_map(&mapA, A, p.T, p.K, S::kTok)) return cudaErrorInvalidValue;
+    if (!code_map(&mapW, W, p.N, p.K, kChan, S::kRowBytes) || !code_map(&mapA, A, p.T, p.K, S::kTok, S::kRowBytes))
+        return cudaErrorInvalidValue;
 
-    const int sms = device_sm_count(), pairs = (p.K / 2 + 2 * kStepBytes - 1) / (2 * kStepBytes);
+    const int sms = device_sm_count(), pairs = (p.K + 511) / 512;
     int ranks = 1;
     if (S::kSplit)  // CTAs that share a tile: as many as still fit the GPU, and have work
         while (ranks < 8 && (ranks + 1) * tiles <= sms && ranks < pairs) ++ranks;
@@ -585,9 +603,9 @@ cudaError_t product(const uint8_t* A, const uint8_t* W, ProductArgs p, cudaStrea
     return cudaLaunchKernelEx(&cfg, kernel, mapW, mapA, p);
 }
 
-using Split16 = ProductShape<16, 9, true>;
-using Split64 = ProductShape<64, 6, true>;
-using Whole192 = ProductShape<192, 4, false>;
+using Split16 = ProductShape<16, 128, 9, true>;
+using Split64 = ProductShape<64, 128, 6, true>;
+using Whole192 = ProductShape<192, 128, 4, false>;
 
 template <bool kMix>
 cudaError_t product_by_size(const uint8_t* A, const uint8_t* W, const ProductArgs& p, cudaStream_t s)

@@ -138,12 +138,15 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16])
 
 // --------------------------------------------------------------- tcgen05 work
 
-// Descriptor of an operand tile in shared memory: rows of 128 bytes along K, in
-// groups of eight rows under the 128-byte swizzle that TMA wrote them with.
+// Descriptor of an operand tile in shared memory: rows of kRowBytes (128 or 64)
+// along K, in groups of eight rows under the swizzle of that width that TMA
+// wrote them with.
+template <int kRowBytes>
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
 {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)2 << 61;
+    static_assert(kRowBytes == 128 || kRowBytes == 64, "swizzle width");
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(8 * kRowBytes >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)(kRowBytes == 128 ? 2 : 4) << 61;
 }
 // Descriptor of 32 rows of 16 bytes, unswizzled, for a copy of scales.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr)
