@@ -510,32 +510,30 @@ def _mx_format(fmt, allowed=("int8", "e4m3", "e2m1")):
 def _mx_empty(like, shape, fmt):
     """An unwritten MxTensor of `shape` beside a tensor."""
     C = shape[-1]
-    rows = tuple(shape[:-1])
     if fmt == "e2m1":
-        codes = like.new_empty(rows + (C // 2,), dtype=torch.uint8)
+        codes = like.new_empty((*shape[:-1], C // 2), dtype=torch.uint8)
     elif like.shape == shape:
         codes = torch.empty_like(like, dtype=torch.uint8)
     else:
         codes = like.new_empty(shape, dtype=torch.uint8)
-    return MxTensor(codes, like.new_empty(rows + (4 * ((C + 127) // 128),), dtype=torch.uint8), fmt)
+    return MxTensor(codes, like.new_empty((*shape[:-1], 4 * ((C + 127) // 128)), dtype=torch.uint8), fmt)
 
 
 def _need_mx(mx, name, allowed, shape=None):
     """Checks a MxTensor and returns the shape that it stands for."""
-    if not isinstance(mx, MxTensor):
+    if type(mx) is not MxTensor:
         raise TypeError("%s must be an MxTensor" % name)
     codes, scales, fmt = mx
     if fmt not in allowed:
         _mx_format(fmt, allowed)
-    _need(codes, name + ".codes", torch.uint8)
-    s = tuple(codes.shape)
+    s = tuple(_need(codes, name, torch.uint8).shape)
     if not s:
         raise ValueError("%s.codes must have at least one dimension" % name)
     if fmt == "e2m1":
-        s = s[:-1] + (2 * s[-1],)
+        s = (*s[:-1], 2 * s[-1])
     if shape is not None and s != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), s))
-    _need(scales, name + ".scales", torch.uint8, s[:-1] + (mx_scale_pitch(s[-1]),))
+    _need(scales, name, torch.uint8, (*s[:-1], 4 * ((s[-1] + 127) // 128)))
     return s
 
 
@@ -547,10 +545,14 @@ def _launch(f, tensors, *numbers):
     the numbers, on the current stream of the tensors' device: they must share
     one, which is made current for the launch if it is not."""
     dev = tensors[0].get_device()
+    ptrs = []
     for t in tensors:
-        if t is not None and t.get_device() != dev:
+        if t is None:
+            ptrs.append(None)
+        elif t.get_device() == dev:
+            ptrs.append(t.data_ptr())
+        else:
             raise ValueError("tensors are on %s and %s" % (tensors[0].device, t.device))
-    ptrs = [None if t is None else t.data_ptr() for t in tensors]
     # the handle behind torch.cuda.current_stream(dev).cuda_stream, without the
     # Stream object: small calls are bound by this thread
     stream = torch._C._cuda_getCurrentRawStream(dev)

@@ -607,11 +607,17 @@ using Split16 = ProductShape<16, 128, 9, true>;
 using Split64 = ProductShape<64, 128, 6, true>;
 using Whole192 = ProductShape<192, 128, 4, false>;
 
+// The form by size.  Split forms run one wave of clusters, so they are taken
+// while their tiles fit the GPU at once, and the narrowest that holds the
+// tokens: at N = 8192, K = 4096 one token takes 7.9 us in tiles of 16 and
+// 9.2 in tiles of 64, 128 tokens take 9.7 us in tiles of 64 (128 tiles) and
+// 11.0 whole, 200 tokens 17.6 (256 tiles, two waves) and 11.9 whole.
 template <bool kMix>
 cudaError_t product_by_size(const uint8_t* A, const uint8_t* W, const ProductArgs& p, cudaStream_t s)
 {
-    if (p.T <= 16) return product<Split16, kMix>(A, W, p, s);
-    if (p.T <= 64) return product<Split64, kMix>(A, W, p, s);
+    const int64_t chan_tiles = (p.N + kChan - 1) / kChan, sms = device_sm_count();
+    if (p.T <= 16 && chan_tiles <= sms) return product<Split16, kMix>(A, W, p, s);
+    if (chan_tiles * ((p.T + 63) / 64) <= sms) return product<Split64, kMix>(A, W, p, s);
     return product<Whole192, kMix>(A, W, p, s);
 }
 
