@@ -82,6 +82,7 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 // NaN in the outputs that are not done.
 
 constexpr int kChan = 128;      // channels of a tile
+constexpr int kRowBytes = 128;  // of K of a tile: 256 elements
 constexpr int kProdThreads = 416;  // 13 warps, four on one scheduler: 128 registers a thread at most
 constexpr int kEpiWarps = 8;
 constexpr int kEpiThreads = 32 * kEpiWarps;
@@ -100,26 +101,25 @@ struct ProductArgs {
     int chan_tiles, tok_tiles;
 };
 
-template <int kTok_, int kRowBytes_, int kStages_, bool kSplit_>
+template <int kTok_, int kStages_, bool kSplit_>
 struct ProductShape {
     static constexpr int kTok = kTok_, kStages = kStages_;
-    static constexpr int kRowBytes = kRowBytes_;  // bytes of K of a tile: twice as many elements
     static constexpr bool kSplit = kSplit_;
     static constexpr int kTokChunks = (kTok + 127) / 128;  // 128-row chunks of A's scales
     static constexpr int kWBytes = kChan * kRowBytes, kABytes = kTok * kRowBytes;
     static constexpr int kStageBytes = kWBytes + kABytes;
-    // scales: two buffers of eight steps of 128 elements, a step's being one
-    // chunk of W's and kTokChunks of A's
-    static constexpr int kSteps = kRowBytes / 64;  // steps of 128 elements in a K tile
-    static constexpr int kBufTiles = 8 / kSteps;
-    static constexpr int kScaleStep = 512 * (1 + kTokChunks), kScaleBytes = 2 * 8 * kScaleStep;
+    // scales: two buffers of kBufTiles K tiles, each tile two steps of 128
+    // elements, a step's being one chunk of W's and kTokChunks of A's
+    static constexpr int kBufTiles = 4, kBufSteps = 2 * kBufTiles;
+    static constexpr int kScaleStep = 512 * (1 + kTokChunks), kScaleBytes = 2 * kBufSteps * kScaleStep;
     static constexpr int kSums = kSplit ? 1 : 2;  // accumulator tiles
     // the epilogue's: two buffers of 32 tokens, or the whole tile's partial sums
-    static constexpr int kEpiBytes = (kSplit ? kTok : 64) * kChan * 4;
+    static constexpr int kGroup = 32;
+    static constexpr int kEpiBytes = (kSplit ? kTok : 2 * kGroup) * kChan * 4;
     static constexpr int kBars = 2 * kStages + 4 + 2 * kSums + 1;
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kScaleBytes + kEpiBytes + 8 * kBars + 16;
     // columns of tensor memory: sums, then each stage's scales of W and A
-    static constexpr int kScaleCols = kSteps * 4 * (1 + kTokChunks);
+    static constexpr int kScaleCols = 8 * (1 + kTokChunks);
     static constexpr int kSumCols = (kSums * kTok + 31) / 32 * 32;
     static constexpr int kColumns = 512;
     static_assert(kSumCols + kStages * kScaleCols <= kColumns, "tensor memory");
@@ -171,17 +171,31 @@ __device__ __forceinline__ uint32_t scales_within(uint32_t word, int w, int KB)
     return left >= 4 ? word : left <= 0 ? 0u : word & (0xffffffffu >> (8 * (4 - left)));
 }
 
-// Eight channels of a token: vector v of N / 8.
+// What the output of eight channels of a token (vector v of N / 8) takes beside
+// the product: nothing, or the mix's streams and maps, loaded ahead.
 template <bool kMix>
-__device__ __forceinline__ void emit(const ProductArgs& p, const float (&f)[8], int64_t t, int v)
-{
-    const int NV = p.N >> 3;
-    if constexpr (kMix) {
-        uint4 x[4];
+struct StreamVec {
+    __device__ __forceinline__ void load(const ProductArgs&, int64_t, int) {}
+    __device__ __forceinline__ void emit(const ProductArgs& p, const float (&f)[8], int64_t t, int v) const
+    {
+        p.out[t * (p.N >> 3) + v] = pack8(f);
+    }
+};
+template <>
+struct StreamVec<true> {
+    uint4 x[4];
+    float h[16], hp[4];
+    __device__ __forceinline__ void load(const ProductArgs& p, int64_t t, int v)
+    {
+        const int NV = p.N >> 3;
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = __ldcs(p.X + (t * 4 + j) * NV + v);
-        float h[16], hp[4], xf[4][8];
         load_maps(p.H, p.hpost, t, h, hp);
+    }
+    __device__ __forceinline__ void emit(const ProductArgs& p, const float (&f)[8], int64_t t, int v) const
+    {
+        const int NV = p.N >> 3;
+        float xf[4][8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) unpack8(x[j], xf[j]);
 #pragma unroll
@@ -196,10 +210,8 @@ __device__ __forceinline__ void emit(const ProductArgs& p, const float (&f)[8], 
             }
             __stcs(p.out + (t * 4 + i) * NV + v, pack8(o));
         }
-    } else {
-        p.out[t * NV + v] = pack8(f);
     }
-}
+};
 
 template <class S, bool kMix>
 __global__ void __launch_bounds__(kProdThreads, 1)
@@ -258,9 +270,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
     const int ranks = S::kSplit ? (int)tc5::cluster_size() : 1, rank = S::kSplit ? (int)tc5::cluster_rank() : 0;
     const int pairs = (p.K + 511) / 512;  // 16 bytes of scales
     const int pair0 = pairs * rank / ranks, pair1 = pairs * (rank + 1) / ranks;
-    constexpr int kPairTiles = 256 / S::kRowBytes;
-    const int ktiles = (p.K / 2 + S::kRowBytes - 1) / S::kRowBytes;
-    const int k0 = kPairTiles * pair0, k1 = min(kPairTiles * pair1, ktiles);
+    const int k0 = 2 * pair0, k1 = min(2 * pair1, (p.K + 255) / 256);
     const int tiles = p.chan_tiles * p.tok_tiles;
     const int first = blockIdx.x / ranks, stride = gridDim.x / ranks;
     bool ok = true;
@@ -277,8 +287,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 const uint32_t at = base + s * S::kStageBytes;
                 if (tc5::elect_one()) {
                     tc5::mbar_expect_tx(full(s), S::kWBytes + S::kABytes);
-                    tc5::tma_load_2d(at, &mapW, k * S::kRowBytes, n0, full(s));
-                    tc5::tma_load_2d(at + kOffA, &mapA, k * S::kRowBytes, t0, full(s));
+                    tc5::tma_load_2d(at, &mapW, k * kRowBytes, n0, full(s));
+                    tc5::tma_load_2d(at + kOffA, &mapA, k * kRowBytes, t0, full(s));
                 }
                 __syncwarp();
                 s = s + 1 == kStages ? 0 : s + 1;
@@ -300,12 +310,12 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 if (j == 0 && !(ok = tc5::mbar_wait_warp(scales_full(buf), par, abort))) break;
                 if (!(ok = tc5::mbar_wait_warp(empty(s), phase ^ 1, abort))) break;
                 tc5::fence_after_sync();
-                const uint32_t at = base + kOffScales + (buf * 8 + j * S::kSteps) * S::kScaleStep;
+                const uint32_t at = base + kOffScales + (buf * S::kBufSteps + 2 * j) * S::kScaleStep;
                 const uint32_t sw = tmem + S::kSumCols + s * S::kScaleCols;
                 const bool last = j + 1 == S::kBufTiles || k + 1 == steps;
                 if (tc5::elect_one()) {
 #pragma unroll
-                    for (int c = 0; c < S::kSteps * (1 + S::kTokChunks); ++c)
+                    for (int c = 0; c < 2 * (1 + S::kTokChunks); ++c)
                         tc5::copy_scales(sw + 4 * c, tc5::scale_desc(at + 512 * c));
                     tc5::commit(full(s));
                     if (last) tc5::commit(scales_empty(buf));
@@ -339,11 +349,11 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 tc5::fence_after_sync();
                 const uint32_t at = base + s * S::kStageBytes;
                 const uint32_t sc = tmem + S::kSumCols + s * S::kScaleCols;
-                const uint64_t dw = tc5::operand_desc<S::kRowBytes>(at);
-                const uint64_t da = tc5::operand_desc<S::kRowBytes>(at + kOffA);
+                const uint64_t dw = tc5::operand_desc(at);
+                const uint64_t da = tc5::operand_desc(at + kOffA);
                 if (tc5::elect_one()) {
 #pragma unroll
-                    for (int q = 0; q < 2 * S::kSteps; ++q) {  // 64 elements: 32 bytes along the swizzled row
+                    for (int q = 0; q < 4; ++q) {  // 64 elements: 32 bytes along the swizzled row
                         const uint32_t sw = sc + 4 * (1 + S::kTokChunks) * (q >> 1);
                         tc5::mma_mx4(d, dw + 2 * q, da + 2 * q, inst | tc5::scale_select(2 * (q & 1)), sw, sw + 4,
                                      k > 0 || q > 0);
@@ -392,12 +402,13 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         fetch(first, pair0);
         for (int tile = first; tile < tiles && ok; tile += stride) {
             for (int pair = pair0; pair < pair1 && ok; pair += 2) {
-                if (!(ok = tc5::mbar_wait(scales_empty(buf), par ^ 1, abort))) break;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {  // steps of 128 elements, one word of scales a row
                     const int w0 = 4 * pair + j;
                     if (pair + j / 4 >= pair1) break;
-                    uint8_t* at = smem + kOffScales + (buf * 8 + j) * S::kScaleStep + (isW ? 0 : 512);
+                    const int at_step = j % S::kBufSteps;
+                    if (at_step == 0 && !(ok = tc5::mbar_wait(scales_empty(buf), par ^ 1, abort))) break;
+                    uint8_t* at = smem + kOffScales + (buf * S::kBufSteps + at_step) * S::kScaleStep + (isW ? 0 : 512);
 #pragma unroll
                     for (int c = 0; c < (kGroups + 3) / 4; ++c) {
                         if (4 * c >= groups) break;
@@ -414,16 +425,18 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                         }
                         reinterpret_cast<uint4*>(at + 512 * c)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                    if (at_step + 1 == S::kBufSteps || (j == 3 && pair + 1 >= pair1)) {  // the buffer's last
+                        tc5::fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) tc5::mbar_arrive(scales_full(buf));
+                        buf ^= 1;
+                        par ^= buf == 0;
+                    }
                 }
-                tc5::fence_async_shared();
-                __syncwarp();
-                if (lane == 0) tc5::mbar_arrive(scales_full(buf));
                 if (pair + 2 < pair1)
                     fetch(tile, pair + 2);
                 else
                     fetch(tile + stride, pair0);
-                buf ^= 1;
-                par ^= buf == 0;
             }
         }
         if (!ok) *abort = 1;
@@ -448,34 +461,49 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
             if (ok) ok = tc5::mbar_wait(sum_full(a), n / S::kSums & 1, abort);
             __syncwarp();
             tc5::fence_after_sync();
-            constexpr int kGroup = 32;  // tokens between two barriers of the epilogue
+            if (S::kSplit) {
+                // each token in its place, for the cluster to add up
 #pragma unroll 1
-            for (int g = 0; g < kTok; g += kGroup) {
-                if (g + 16 * half < kTok) {
+                for (int g = 16 * half; g < kTok; g += 32) {
                     float v[16];
-                    tc5::tmem_load16(tmem + row + a * kTok + g + 16 * half, v);
-                    // whole: two buffers in turn; split: each token in its place
-                    float* to = epi + ((S::kSplit ? g : g & kGroup) + 16 * half) * kChan + 32 * quarter + lane;
+                    tc5::tmem_load(tmem + row + a * kTok + g, v);
+                    float* to = epi + g * kChan + 32 * quarter + lane;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) to[i * kChan] = ok ? v[i] : __int_as_float(0x7fffffff);
                 }
-                if (!S::kSplit) {
-                    if (g + kGroup >= kTok) {  // the last read of this tile's sums
+            } else {
+#pragma unroll 1
+                for (int g = 0; g < kTok; g += S::kGroup) {
+                    // this thread's eight channels of two tokens of the group
+                    const int vec = v0 + (e & 15);
+                    StreamVec<kMix> x[2];
+                    bool in[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int64_t t = t0 + g + (e >> 4) + 16 * i;
+                        in[i] = t < p.T && 8 * vec < p.N;
+                        if (in[i]) x[i].load(p, t, vec);
+                    }
+                    float v[16];
+                    tc5::tmem_load(tmem + row + a * kTok + g + 16 * half, v);
+                    if (g + S::kGroup >= kTok) {  // the last read of this tile's sums
                         tc5::fence_before_sync();
                         __syncwarp();
                         if (lane == 0) tc5::mbar_arrive(sum_empty(a));
                     }
+                    // two buffers in turn: by the barrier of the next group, all have read this one
+                    float* buf = epi + (g & S::kGroup) * kChan;
+                    float* to = buf + 16 * half * kChan + 32 * quarter + lane;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) to[i * kChan] = ok ? v[i] : __int_as_float(0x7fffffff);
                     asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
 #pragma unroll
-                    for (int i = e; i < kGroup * (kChan / 8); i += kEpiThreads) {
-                        const int tok = i >> 4, v = i & 15;
-                        const int64_t t = t0 + g + tok;
-                        if (t < p.T && g + tok < kTok && 8 * (v0 + v) < p.N) {
-                            const float4* q = reinterpret_cast<const float4*>(epi + ((g & kGroup) + tok) * kChan) + 2 * v;
-                            const float4 lo = q[0], hi = q[1];
-                            const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                            emit<kMix>(p, f, t, v0 + v);
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        if (!in[i]) continue;
+                        const float4* q = reinterpret_cast<const float4*>(buf + ((e >> 4) + 16 * i) * kChan) + 2 * (e & 15);
+                        const float4 lo = q[0], hi = q[1];
+                        const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        x[i].emit(p, f, t0 + g + (e >> 4) + 16 * i, vec);
                     }
                 }
             }
@@ -494,6 +522,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         for (int i = rank * kProdThreads + threadIdx.x; i < kItems; i += ranks * kProdThreads) {
             const int tok = i >> 4, v = i & 15;
             if (t0 + tok < p.T && 8 * (v0 + v) < p.N) {
+                StreamVec<kMix> x;
+                x.load(p, t0 + tok, v0 + v);
                 float f[8] = {};
                 for (int r = 0; r < ranks; ++r) {
                     const uint32_t at = tc5::map_rank(tc5::smem_addr(epi + tok * kChan + 8 * v), r);
@@ -502,7 +532,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
 #pragma unroll
                     for (int x = 0; x < 8; ++x) f[x] += q[x];
                 }
-                emit<kMix>(p, f, t0 + tok, v0 + v);
+                x.emit(p, f, t0 + tok, v0 + v);
             }
         }
         tc5::cluster_sync();  // nobody's shared memory goes while it may be read
@@ -529,7 +559,7 @@ cudaError_t launch_premap_fwd_mx4(const uint16_t* X, const float* hpre, uint8_t*
 
 namespace {
 
-// A byte matrix [rows][pitch] read in boxes of box_rows x box_bytes (128 or 64).
+// A byte matrix [rows][pitch] read in boxes of box_rows x 128 bytes.
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -551,14 +581,13 @@ EncodeTiled encode_tiled()
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-bool code_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box_rows, int box_bytes)
+bool code_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box_rows)
 {
     const EncodeTiled f = encode_tiled();
     const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(K / 2)};
-    const cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {kRowBytes, (cuuint32_t)box_rows}, step[2] = {1, 1};
     return f != nullptr && f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box,
-                             step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                             box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -580,8 +609,7 @@ cudaError_t product(const uint8_t* A, const uint8_t* W, ProductArgs p, cudaStrea
     const int64_t tiles = (int64_t)p.chan_tiles * p.tok_tiles;
     if (tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
     CUtensorMap mapW, mapA;
-    if (!code_map(&mapW, W, p.N, p.K, kChan, S::kRowBytes) || !code_map(&mapA, A, p.T, p.K, S::kTok, S::kRowBytes))
-        return cudaErrorInvalidValue;
+    if (!code_map(&mapW, W, p.N, p.K, kChan) || !code_map(&mapA, A, p.T, p.K, S::kTok)) return cudaErrorInvalidValue;
 
     const int sms = device_sm_count(), pairs = (p.K + 511) / 512;
     int ranks = 1;
@@ -603,9 +631,9 @@ cudaError_t product(const uint8_t* A, const uint8_t* W, ProductArgs p, cudaStrea
     return cudaLaunchKernelEx(&cfg, kernel, mapW, mapA, p);
 }
 
-using Split16 = ProductShape<16, 128, 9, true>;
-using Split64 = ProductShape<64, 128, 6, true>;
-using Whole192 = ProductShape<192, 128, 4, false>;
+using Split16 = ProductShape<16, 9, true>;
+using Split64 = ProductShape<64, 6, true>;
+using Whole192 = ProductShape<192, 4, false>;
 
 // The form by size.  Split forms run one wave of clusters, so they are taken
 // while their tiles fit the GPU at once, and the narrowest that holds the

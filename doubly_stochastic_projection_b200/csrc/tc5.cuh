@@ -120,11 +120,11 @@ __device__ __forceinline__ void fence_before_sync()
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
 
-// 16 consecutive columns of the warp's 32 lanes, one lane a thread.
-__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16])
+// 16 consecutive columns of the warp's 32 lanes, one lane a thread.  One
+// statement with its wait, so that no use of the registers can come before it.
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[16])
 {
     uint32_t r[16];
-    // one statement, so that no use of the registers can come before the wait
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
                  "tcgen05.wait::ld.sync.aligned;"
@@ -135,18 +135,14 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16])
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-
 // --------------------------------------------------------------- tcgen05 work
 
-// Descriptor of an operand tile in shared memory: rows of kRowBytes (128 or 64)
-// along K, in groups of eight rows under the swizzle of that width that TMA
-// wrote them with.
-template <int kRowBytes>
+// Descriptor of an operand tile in shared memory: rows of 128 bytes along K, in
+// groups of eight rows under the 128-byte swizzle that TMA wrote them with.
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
 {
-    static_assert(kRowBytes == 128 || kRowBytes == 64, "swizzle width");
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(8 * kRowBytes >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)(kRowBytes == 128 ? 2 : 4) << 61;
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
 }
 // Descriptor of 32 rows of 16 bytes, unswizzled, for a copy of scales.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr)
