@@ -65,13 +65,14 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 // columns) and walks K in tiles of 256 elements, 128 bytes a row.  Its warps:
 //   0     loads the code tiles by TMA (128-byte swizzle) into a ring of stages
 //   1     issues the products, four steps of 64 a tile
-//   2, 3  bring the scales of W and A.  They are rows of bytes in memory and
-//         have to be, for the tensor cores, chunks of 512 bytes with the four
-//         bytes of rows r, r + 32, r + 64, r + 96 side by side: a lane reads 16
-//         bytes (two tiles' worth) of four rows and stores four 16-byte vectors
+//   2     issues the copies of the scales into tensor memory
+//   3, 12, ...  bring the scales, one warp for each chunk of 128 rows of W or
+//         A.  They are rows of bytes in memory and have to be, for the tensor
+//         cores, chunks of 512 bytes with the four bytes of rows r, r + 32,
+//         r + 64, r + 96 side by side: a lane reads 32 bytes (four tiles' worth)
+//         of four rows, a round ahead, and stores 16-byte vectors
 //   4-11  the epilogue: tensor memory -> shared memory, turned so that a
 //         thread holds eight consecutive channels of a token -> the output
-//   12    issues the copies of the scales into tensor memory
 // Two forms.  Whole: one persistent CTA an SM walks output tiles, the sums of
 // one tile in one half of tensor memory while the epilogue drains the other.
 // Split: a cluster shares one output tile, each CTA a part of K; the partial
@@ -83,7 +84,6 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 
 constexpr int kChan = 128;      // channels of a tile
 constexpr int kRowBytes = 128;  // of K of a tile: 256 elements
-constexpr int kProdThreads = 416;  // 13 warps, four on one scheduler: 128 registers a thread at most
 constexpr int kEpiWarps = 8;
 constexpr int kEpiThreads = 32 * kEpiWarps;
 
@@ -106,6 +106,7 @@ struct ProductShape {
     static constexpr int kTok = kTok_, kStages = kStages_;
     static constexpr bool kSplit = kSplit_;
     static constexpr int kTokChunks = (kTok + 127) / 128;  // 128-row chunks of A's scales
+    static constexpr int kThreads = 32 * (12 + kTokChunks);  // four warps a scheduler: 128 registers at most
     static constexpr int kWBytes = kChan * kRowBytes, kABytes = kTok * kRowBytes;
     static constexpr int kStageBytes = kWBytes + kABytes;
     // scales: two buffers of kBufTiles K tiles, each tile two steps of 128
@@ -214,7 +215,7 @@ struct StreamVec<true> {
 };
 
 template <class S, bool kMix>
-__global__ void __launch_bounds__(kProdThreads, 1)
+__global__ void __launch_bounds__(S::kThreads, 1)
 mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapA,
                    const ProductArgs p)
 {
@@ -248,7 +249,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
             tc5::mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
-            tc5::mbar_init(scales_full(b), 2);  // the two scale warps
+            tc5::mbar_init(scales_full(b), 1 + S::kTokChunks);  // the scale warps
             tc5::mbar_init(scales_empty(b), 1);
         }
         for (int a = 0; a < S::kSums; ++a) {
@@ -300,7 +301,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
             for (int64_t j = loads > kStages ? loads - kStages : 0; j < loads; ++j)
                 tc5::mbar_wait(full((int)(j % kStages)), (uint32_t)(j / kStages) & 1, nullptr, kDrainNs);
         }
-    } else if (warp == 12) {
+    } else if (warp == 2) {
         // each K tile's scales from shared into tensor memory, ahead of the products
         int s = 0, buf = 0;
         uint32_t phase = 0, par = 0;
@@ -372,9 +373,11 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
             __syncwarp();
             tc5::mbar_wait(drained, 0, nullptr, kDrainNs);
         }
-    } else if (warp < 4) {
-        // warp 2: W's rows, warp 3: A's; lane l holds rows l, l + 32, ... of the tile
-        const bool isW = warp == 2;
+    } else if (warp == 3 || warp >= 12) {
+        // warp 3: W's rows, the others: 128 of A's each; lane l holds rows l, l + 32,
+        // l + 64 and l + 96 of the chunk
+        const bool isW = warp == 3;
+        const int chunk = isW ? 0 : warp - 11, in_tile = isW ? 0 : 128 * (warp - 12);
         const uint8_t* src = isW ? p.Ws : p.As;
         const int KB = p.K / kMxBlock, pitch = (int)mx_scale_pitch(p.K);
         // of every pair of 512 elements that is fetched together
@@ -382,17 +385,16 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                           : (pitch & 15) == 0                                                                ? 16
                                                                                                              : 4;
         const int64_t rows = isW ? (int64_t)p.N : p.T;
-        constexpr int kGroups = (kTok + 31) / 32 > 4 ? (kTok + 31) / 32 : 4;
-        const int groups = isW ? 4 : (kTok + 31) / 32;
-        // two pairs of K tiles, fetched while the buffers before them are in work
-        uint4 next[2][kGroups];
+        // the round in work, of four K tiles (two pairs), and the next on its way
+        uint4 cur[2][4], next[2][4];
         const auto fetch = [&](int tile, int pair) {
             if (tile >= tiles) return;
-            const int64_t r0 = isW ? (int64_t)(tile % p.chan_tiles) * kChan : (int64_t)(tile / p.chan_tiles) * kTok;
+            const int64_t r0 =
+                isW ? (int64_t)(tile % p.chan_tiles) * kChan : (int64_t)(tile / p.chan_tiles) * kTok + in_tile;
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                if (g >= groups) break;
-                // rows past the end stand in for none: what they give is not written
+            for (int g = 0; g < 4; ++g) {
+                // rows past the end, or past the tile, stand in for none: what they
+                // give is not written
                 const uint8_t* row = src + min(r0 + 32 * g + lane, rows - 1) * pitch;
                 fetch_scales(row, pair, pair + 1 < pair1, pitch, align, next[0][g], next[1][g]);
             }
@@ -403,40 +405,33 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         for (int tile = first; tile < tiles && ok; tile += stride) {
             for (int pair = pair0; pair < pair1 && ok; pair += 2) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {  // steps of 128 elements, one word of scales a row
-                    const int w0 = 4 * pair + j;
-                    if (pair + j / 4 >= pair1) break;
-                    const int at_step = j % S::kBufSteps;
-                    if (at_step == 0 && !(ok = tc5::mbar_wait(scales_empty(buf), par ^ 1, abort))) break;
-                    uint8_t* at = smem + kOffScales + (buf * S::kBufSteps + at_step) * S::kScaleStep + (isW ? 0 : 512);
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int c = 0; c < (kGroups + 3) / 4; ++c) {
-                        if (4 * c >= groups) break;
-                        uint32_t w[4];
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int r = 4 * c + g;
-                            w[g] = 0u;
-                            if (r < kGroups && r < groups) {
-                                const uint4 q = next[j >> 2][r < kGroups ? r : 0];
-                                w[g] = (j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w;
-                            }
-                            if (4 * (w0 + 1) > KB) w[g] = scales_within(w[g], w0, KB);
-                        }
-                        reinterpret_cast<uint4*>(at + 512 * c)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                    if (at_step + 1 == S::kBufSteps || (j == 3 && pair + 1 >= pair1)) {  // the buffer's last
-                        tc5::fence_async_shared();
-                        __syncwarp();
-                        if (lane == 0) tc5::mbar_arrive(scales_full(buf));
-                        buf ^= 1;
-                        par ^= buf == 0;
-                    }
-                }
+                    for (int g = 0; g < 4; ++g) cur[u][g] = next[u][g];
                 if (pair + 2 < pair1)
                     fetch(tile, pair + 2);
                 else
                     fetch(tile + stride, pair0);
+                if (!(ok = tc5::mbar_wait(scales_empty(buf), par ^ 1, abort))) break;
+#pragma unroll
+                for (int j = 0; j < S::kBufSteps; ++j) {  // steps of 128 elements, one word of scales a row
+                    const int w0 = 4 * pair + j;
+                    if (pair + j / 4 >= pair1) break;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint4 q = cur[j >> 2][g];
+                        w[g] = (j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w;
+                        if (4 * (w0 + 1) > KB) w[g] = scales_within(w[g], w0, KB);
+                    }
+                    uint8_t* at = smem + kOffScales + (buf * S::kBufSteps + j) * S::kScaleStep + 512 * chunk;
+                    reinterpret_cast<uint4*>(at)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                tc5::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) tc5::mbar_arrive(scales_full(buf));
+                buf ^= 1;
+                par ^= buf == 0;
             }
         }
         if (!ok) *abort = 1;
@@ -449,15 +444,6 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
             const int a = n % S::kSums;
             const int v0 = tile % p.chan_tiles * (kChan / 8);
             const int64_t t0 = (int64_t)(tile / p.chan_tiles) * kTok;
-            if (kMix) {
-                // the streams of this tile towards L2, while its sums are made:
-                // 128-byte lines, two for each stream of a token
-                for (int i = e; i < kTok * 8; i += kEpiThreads) {
-                    const int64_t t = t0 + (i >> 3);
-                    const int v = v0 + (i & 1) * 8;
-                    if (t < p.T && 8 * v < p.N) prefetch_l2(p.X + (t * 4 + (i >> 1 & 3)) * (p.N >> 3) + v);
-                }
-            }
             if (ok) ok = tc5::mbar_wait(sum_full(a), n / S::kSums & 1, abort);
             __syncwarp();
             tc5::fence_after_sync();
@@ -519,7 +505,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         const int v0 = first % p.chan_tiles * (kChan / 8);
         const int64_t t0 = (int64_t)(first / p.chan_tiles) * kTok;
         constexpr int kItems = kTok * (kChan / 8);
-        for (int i = rank * kProdThreads + threadIdx.x; i < kItems; i += ranks * kProdThreads) {
+        for (int i = rank * S::kThreads + threadIdx.x; i < kItems; i += ranks * S::kThreads) {
             const int tok = i >> 4, v = i & 15;
             if (t0 + tok < p.T && 8 * (v0 + v) < p.N) {
                 StreamVec<kMix> x;
@@ -617,7 +603,7 @@ cudaError_t product(const uint8_t* A, const uint8_t* W, ProductArgs p, cudaStrea
         while (ranks < 8 && (ranks + 1) * tiles <= sms && ranks < pairs) ++ranks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(S::kSplit ? tiles * ranks : tiles < sms ? tiles : sms));
-    cfg.blockDim = dim3(kProdThreads);
+    cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmemBytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
