@@ -367,6 +367,7 @@ struct CkptIn {
 };
 
 constexpr int kStages = 2;
+constexpr int kBwdCtas = 4;  // an SM: 128 registers a thread
 
 template <bool kZCodes>
 struct CkptRing {
@@ -379,7 +380,7 @@ struct CkptRing {
     const uint4* dY;
     CkptIn in;
     int64_t ntok, ik, sp;
-    int CV, per_tok, iq, is, cs;
+    int CV, rounds, iq, is, cs;
 
     __device__ __forceinline__ uint4* vec16(int slot, int r) const
     {
@@ -399,36 +400,41 @@ struct CkptRing {
 
     __device__ __forceinline__ CkptRing(void* smem, const uint4* dY_, const CkptIn& in_, int64_t T, int CV_)
         : slots(static_cast<uint8_t*>(smem)), dY(dY_), in(in_), ik(0), sp(mx_scale_pitch((int64_t)CV_ * 8)), CV(CV_),
-          iq(0), is(0), cs(0)
+          rounds((CV_ + kThreads - 1) / kThreads), iq(0), is(0), cs(0)
     {
-        per_tok = (int)threadIdx.x < CV ? (CV - 1 - (int)threadIdx.x) / kThreads + 1 : 0;
         ntok = (int64_t)blockIdx.x < T ? (T - 1 - (int64_t)blockIdx.x) / gridDim.x + 1 : 0;
 #pragma unroll
         for (int j = 0; j < kStages - 1; ++j) issue();
     }
 
+    // Tokens of this CTA, and rounds of kThreads vectors in each.  Both, and the
+    // ring's place, are the whole CTA's, so that row addresses are uniform; a
+    // thread past the row copies nothing.
     __device__ __forceinline__ int64_t tokens() const { return ntok; }
-    __device__ __forceinline__ int vectors() const { return per_tok; }
+    __device__ __forceinline__ int token_rounds() const { return rounds; }
 
     __device__ __forceinline__ void issue()
     {
-        if (per_tok > 0 && ik < ntok) {
+        if (ik < ntok) {
             const int64_t t = (int64_t)blockIdx.x + ik * gridDim.x;
-            const int v = (int)threadIdx.x + iq * kThreads;
+            const unsigned v = threadIdx.x + iq * kThreads;
+            if ((int)v < CV) {
+                const unsigned w = v >> 4 << 2;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) cp_async16(vec16(is, r), dY + (t * 4 + r) * CV + v);
+                for (int r = 0; r < 4; ++r) cp_async16(vec16(is, r), dY + (t * 4 + r) * CV + v);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                cp_async8(codes(is, r), reinterpret_cast<const uint2*>(in.Xc) + (t * 4 + r) * CV + v);
-                cp_async4(scale4(is, r), in.Xs + (t * 4 + r) * sp + (v >> 4) * 4);
+                for (int r = 0; r < 4; ++r) {
+                    cp_async8(codes(is, r), reinterpret_cast<const uint2*>(in.Xc) + (t * 4 + r) * CV + v);
+                    cp_async4(scale4(is, r), in.Xs + (t * 4 + r) * sp + w);
+                }
+                if (kZCodes) {
+                    cp_async8(codes(is, kCoded - 1), reinterpret_cast<const uint2*>(in.Zc) + t * CV + v);
+                    cp_async4(scale4(is, kCoded - 1), in.Zs + t * sp + w);
+                } else {
+                    cp_async16(vec16(is, kVec16 - 1), in.Z + t * CV + v);
+                }
             }
-            if (kZCodes) {
-                cp_async8(codes(is, kCoded - 1), reinterpret_cast<const uint2*>(in.Zc) + t * CV + v);
-                cp_async4(scale4(is, kCoded - 1), in.Zs + t * sp + (v >> 4) * 4);
-            } else {
-                cp_async16(vec16(is, kVec16 - 1), in.Z + t * CV + v);
-            }
-            if (++iq == per_tok) {
+            if (++iq == rounds) {
                 iq = 0;
                 ++ik;
             }
@@ -461,7 +467,7 @@ struct CkptRing {
 // dX, dF, dH, dh_post and the chained projection backward, X and F restored
 // from their codes in registers.
 template <int kFmt>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBwdCtas)
 mix_bwd_ckpt_kernel(CkptIn in, const float* H, const float* hpost, const uint4* dY, uint4* dX, float* dH,
                     float* dhpost, uint4* dF, float* dlogits, int64_t T, int CV)
 {
@@ -483,9 +489,10 @@ mix_bwd_ckpt_kernel(CkptIn in, const float* H, const float* hpost, const uint4* 
         float acc[20];
 #pragma unroll
         for (int q = 0; q < 20; ++q) acc[q] = 0.0f;
-        for (int q = 0; q < ring.vectors(); ++q) {
+        for (int q = 0; q < ring.token_rounds(); ++q) {
             const int slot = ring.next();
             const int v = tid + q * kThreads;
+            if (v >= CV) continue;
             float dyf[4][8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) unpack8(*ring.vec16(slot, i), dyf[i]);
@@ -572,7 +579,7 @@ mix_post_bwd_ckpt_kernel(const uint4* dY, const uint8_t* Fc, const uint8_t* Fs, 
 // Main part of the split backward with the pre-map's: dX, dH, dh_pre and the
 // chained projection backward, X restored from its codes in registers.
 template <int kFmt>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBwdCtas)
 mix_premap_bwd_ckpt_kernel(CkptIn in, const float* H, const float* hpre, const uint4* dY, uint4* dX, float* dH,
                            float* dhpre, float* dlogits, int64_t T, int CV)
 {
@@ -595,9 +602,10 @@ mix_premap_bwd_ckpt_kernel(CkptIn in, const float* H, const float* hpre, const u
         float acc[20];
 #pragma unroll
         for (int q = 0; q < 20; ++q) acc[q] = 0.0f;
-        for (int u = 0; u < ring.vectors(); ++u) {
+        for (int u = 0; u < ring.token_rounds(); ++u) {
             const int slot = ring.next();
             const int v = tid + u * kThreads;
+            if (v >= CV) continue;
             float dyf[4][8], g[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) unpack8(*ring.vec16(slot, i), dyf[i]);
