@@ -337,8 +337,12 @@ def _product_bound(K, mag):
     return (K // 32 + 8) * 2 * FP32 * mag
 
 
+# the forms of the product: one tile shared along K in tiles of 16 and of 64
+# tokens, and (from 149 tiles of 64 tokens on) persistent tiles of 192
 PRODUCTS = [(1, 8, 32), (1, 136, 512), (2, 264, 96), (7, 1032, 1056), (16, 512, 4096), (17, 520, 2048), (33, 128, 256),
-            (64, 4104, 320), (65, 384, 288), (129, 256, 1024), (200, 1000, 544), (257, 136, 4128), (1030, 200, 352)]
+            (64, 4104, 320), (65, 384, 288), (129, 256, 1024), (200, 1000, 544), (257, 136, 4128), (1030, 200, 352),
+            (1, 19000, 512), (16, 18952, 96), (200, 8200, 1056), (513, 2200, 1024), (2500, 520, 544), (700, 4104, 4128),
+            (9600, 136, 256), (385, 3080, 1536)]
 
 
 @pytest.mark.parametrize("T,N,K", PRODUCTS)
@@ -369,6 +373,29 @@ def test_product_with_mix(T, C, K):
     assert (np.abs(to_np64(got) - ref) <= tol).all()
     assert (out[T:] == 7).all()
     assert torch.equal(got, api.mx4_linear_mix(a, w, X, H, h))
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 264, 2048), (300, 6200, 2048)])
+def test_product_of_operands_on_sixteen_byte_boundaries(T, N, K):
+    a, w = _operands(T, N, K, 5)
+
+    def moved(t):
+        flat = torch.empty(t.numel() + 16, dtype=torch.uint8, device=dev())[16:]
+        assert flat.data_ptr() % 32 == 16
+        return flat.view(t.shape).copy_(t)
+
+    b, v = (api.MxTensor(moved(q.codes), moved(q.scales), q.fmt) for q in (a, w))
+    out = torch.empty(T * N + 8, dtype=torch.bfloat16, device=dev())[8:].view(T, N)
+    assert torch.equal(api.mx4_linear(b, v, out=out), api.mx4_linear(a, w))
+
+
+def test_bytes_behind_the_last_scale_do_not_count():
+    # scale rows are padded to four bytes; what a caller left in the padding is not read
+    a, w = _operands(5, 40, 160, 6)
+    ref = api.mx4_linear(a, w)
+    for q in (a, w):
+        q.scales[:, 5:] = 255
+    assert torch.equal(api.mx4_linear(a, w), ref)
 
 
 def test_product_of_special_blocks():
