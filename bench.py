@@ -85,7 +85,9 @@ def parse():
     ap.add_argument("--profile", default=None,
                     choices=["newton_fwd", "sinkhorn_fwd", "sinkhorn_bwd", "implicit_bwd", "mix_fwd", "mix_bwd",
                              "proj_mix_fwd", "proj_mix_bwd", "premap_fwd", "mix_post_bwd", "mix_premap_bwd",
-                             "newton_fwd_n", "implicit_bwd_n", "composite_gain", "fwd_bwd_mapped"],
+                             "newton_fwd_n", "implicit_bwd_n", "composite_gain", "fwd_bwd_mapped",
+                             "mx_pack", "mx_unpack", "mix_fwd_ckpt", "mix_bwd_ckpt", "mix_post_bwd_ckpt",
+                             "mix_premap_bwd_ckpt", "premap_fwd_mx4", "mx4_linear", "mx4_linear_mix"],
                     help="run one kernel --reps times on one case (for ncu) and exit")
     ap.add_argument("--method", default="newton", help="--profile newton_fwd: projection method")
     ap.add_argument("--layout", default="auto", choices=["auto", "thread", "lane_pair", "row_group"],
@@ -94,6 +96,9 @@ def parse():
     ap.add_argument("--channels", type=int, default=4096, help="--profile: mix channels C")
     ap.add_argument("--dist", default="normal1", help="--profile: logit distribution")
     ap.add_argument("--n", type=int, default=8, help="--profile newton_fwd_n / implicit_bwd_n: matrix size")
+    ap.add_argument("--format", default="int8", choices=["int8", "e4m3", "e2m1"],
+                    help="--profile mx_*, *_ckpt: microscaled format")
+    ap.add_argument("--inner", type=int, default=4096, help="--profile mx4_linear*: the product's inner size K")
     ap.add_argument("--reps", type=int, default=3)
     return ap.parse_args()
 
@@ -979,6 +984,18 @@ def run_profile_case(args):
               "sinkhorn_bwd": lambda: api.sinkhorn_bwd(G, A, 20),
               "implicit_bwd": lambda: api.birkhoff_bwd(G, P=P, out=out)}[k]
         desc = {"n_mats": n, "dist": args.dist, "method": args.method, "layout": args.layout}
+    elif k in ("mx4_linear", "mx4_linear_mix"):
+        T, N, K = args.size, args.channels, args.inner
+        a = api.mx_pack(inputs.bf16_normal((T, K), 30, dev), "e2m1")
+        w = api.mx_pack(inputs.bf16_normal((N, K), 31, dev), "e2m1")
+        if k == "mx4_linear":
+            fn = lambda: api.mx4_linear(a, w)
+        else:
+            m = inputs.mix_workload("mix_T16384_C4096", device=dev, T=T, C=N)
+            H = api.birkhoff_fwd(torch.from_numpy(m["logits"]).to(dev), "newton")
+            h = torch.from_numpy(m["h_post"]).to(dev)
+            fn = lambda: api.mx4_linear_mix(a, w, m["X"], H, h)
+        desc = {"T": T, "N": N, "K": K}
     else:
         m = inputs.mix_workload("mix_T16384_C4096", device=dev, T=args.size, C=args.channels)
         X, F, dY = m["X"], m["F"], m["dY"]
@@ -988,7 +1005,16 @@ def run_profile_case(args):
         Y = torch.empty_like(X)
         hpre = torch.from_numpy(inputs.h_post(args.size, 17)).to(dev) - 1.0
         dx_in = dY[:, 0, :].contiguous()
-        fn = {"mix_fwd": lambda: api.residual_mix_fwd(X, H, h, F, out=Y),
+        if k in ("mx_unpack", "mix_bwd_ckpt", "mix_post_bwd_ckpt", "mix_premap_bwd_ckpt"):
+            Xq, Fq = api.mx_pack(X, args.format), api.mx_pack(F, args.format)
+        fn = {"mx_pack": lambda: api.mx_pack(X, args.format),
+              "mx_unpack": lambda: api.mx_unpack(Xq, out=Y),
+              "mix_fwd_ckpt": lambda: api.residual_mix_fwd_ckpt(X, H, h, F, args.format, out=Y),
+              "mix_bwd_ckpt": lambda: api.residual_mix_bwd_ckpt(Xq, H, h, Fq, dY, need_dlogits=True),
+              "mix_post_bwd_ckpt": lambda: api.mix_post_bwd_ckpt(dY, Fq, h),
+              "mix_premap_bwd_ckpt": lambda: api.mix_premap_bwd_ckpt(Xq, H, hpre, dY, dx_in),
+              "premap_fwd_mx4": lambda: api.premap_fwd_mx4(X, hpre),
+              "mix_fwd": lambda: api.residual_mix_fwd(X, H, h, F, out=Y),
               "mix_bwd": lambda: api.residual_mix_bwd(X, H, h, F, dY, need_dlogits=True),
               "proj_mix_fwd": lambda: api.proj_mix_fwd(lg, h, X, F, out=Y, H_out=H),
               "proj_mix_bwd": lambda: api.proj_mix_bwd(H, h, X, F, dY),
@@ -996,6 +1022,8 @@ def run_profile_case(args):
               "mix_post_bwd": lambda: api.mix_post_bwd(dY, F, h),
               "mix_premap_bwd": lambda: api.mix_premap_bwd(X, H, hpre, dY, dx_in)}[k]
         desc = {"T": args.size, "C": args.channels}
+        if k.startswith("mx_") or k.endswith("_ckpt"):
+            desc["format"] = args.format
     for _ in range(args.reps):
         fn()
     torch.cuda.synchronize()

@@ -19,8 +19,9 @@
  *  - All tensor pointers are DEVICE pointers owned by the caller (the one
  *    exception, mhc_birkhoff_fwd_bwd_host, also takes pinned host buffers).
  *    The library allocates no memory, frees nothing and keeps no state
- *    between calls apart from a per-device cache of the SM count and the two
- *    copy streams (with their events) of mhc_birkhoff_fwd_bwd_host.
+ *    between calls apart from a per-device cache of the SM count and of kernel
+ *    attributes, and the two copy streams (with their events) of
+ *    mhc_birkhoff_fwd_bwd_host.
  *  - Every call is asynchronous on `stream` (a cudaStream_t passed as void*;
  *    NULL means the legacy default stream) and returns as soon as the work is
  *    enqueued.
