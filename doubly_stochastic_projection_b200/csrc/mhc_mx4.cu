@@ -341,30 +341,40 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         constexpr uint32_t inst = tc5::mx4_instruction(kChan, kTok);
         int s = 0;
         uint32_t phase = 0;
+        if (mine > 0) ok = tc5::mbar_wait_warp(full(0), 0, abort);
         for (int n = 0; n < mine && ok; ++n) {
             const int a = n % S::kSums;
             if (!(ok = tc5::mbar_wait_warp(sum_empty(a), (n / S::kSums & 1) ^ 1, abort))) break;
             const uint32_t d = tmem + a * kTok;
             for (int k = 0; k < steps; ++k) {
-                if (!(ok = tc5::mbar_wait_warp(full(s), phase, abort))) break;
                 tc5::fence_after_sync();
                 const uint32_t at = base + s * S::kStageBytes;
                 const uint32_t sc = tmem + S::kSumCols + s * S::kScaleCols;
-                const uint64_t dw = tc5::operand_desc(at);
-                const uint64_t da = tc5::operand_desc(at + kOffA);
+                const uint64_t dw = tc5::operand_desc(at), da = tc5::operand_desc(at + kOffA);
+                const int here = s;
+                s = s + 1 == kStages ? 0 : s + 1;
+                phase ^= s == 0;
+                // 64 elements a step, 32 bytes along the swizzled row
+                const auto step = [&](int q) {
+                    const uint32_t sw = sc + 4 * (1 + S::kTokChunks) * (q >> 1);
+                    tc5::mma_mx4(d, dw + 2 * q, da + 2 * q, inst | tc5::scale_select(2 * (q & 1)), sw, sw + 4,
+                                 k > 0 || q > 0);
+                };
                 if (tc5::elect_one()) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {  // 64 elements: 32 bytes along the swizzled row
-                        const uint32_t sw = sc + 4 * (1 + S::kTokChunks) * (q >> 1);
-                        tc5::mma_mx4(d, dw + 2 * q, da + 2 * q, inst | tc5::scale_select(2 * (q & 1)), sw, sw + 4,
-                                     k > 0 || q > 0);
-                    }
-                    tc5::commit(empty(s));
+                    step(0);
+                    step(1);
+                    step(2);
+                }
+                __syncwarp();
+                // the next K tile's wait, while the queue holds steps of this one
+                if (k + 1 < steps || n + 1 < mine) ok = tc5::mbar_wait_warp(full(s), phase, abort);
+                if (tc5::elect_one()) {
+                    step(3);
+                    tc5::commit(empty(here));
                     if (k + 1 == steps) tc5::commit(sum_full(a));
                 }
                 __syncwarp();
-                s = s + 1 == kStages ? 0 : s + 1;
-                phase ^= s == 0;
+                if (!ok) break;
             }
         }
         if (!ok) {
