@@ -533,3 +533,55 @@ def test_binding_refusals():
     with pytest.raises(api.MhcError) as e:  # N not a multiple of 8
         api.mx4_linear(q4, api.mx_pack(torch.ones((4, 64), dtype=torch.bfloat16, device=d), "e2m1"))
     assert e.value.status == 3
+
+
+# --------------------------------------------------- offsets past 32 bits
+
+def _tail_equals(whole, part, n):
+    return all(torch.equal(w[-n:], p) for w, p in zip(whole, part))
+
+
+def test_offsets_past_32_bits():
+    # streams of 4.9e9 elements: the last tokens come out as they do alone
+    T, C, n = 300_000, 4096, 3
+    d = dev()
+    g = torch.Generator(d).manual_seed(1)
+    X = torch.randn((T, 4, C), generator=g, device=d, dtype=torch.bfloat16)
+    F = torch.randn((T, C), generator=g, device=d, dtype=torch.bfloat16)
+    H, h = torch.rand((T, 4, 4), generator=g, device=d), torch.rand((T, 4), generator=g, device=d)
+    cut = [t[-n:].contiguous() for t in (X, H, h, F)]
+    Y, Xq, Fq = api.residual_mix_fwd_ckpt(X, H, h, F)
+    Y1, Xq1, Fq1 = api.residual_mix_fwd_ckpt(*cut)
+    assert _tail_equals((Y, *Xq[:2], *Fq[:2]), (Y1, *Xq1[:2], *Fq1[:2]), n)
+    q = api.mx_pack(X, "int8")
+    assert torch.equal(q.codes, Xq.codes) and torch.equal(q.scales, Xq.scales)
+    del q
+    torch.cuda.empty_cache()
+    assert torch.equal(api.mx_unpack(Xq)[-n:], api.mx_unpack(Xq1))
+    out = api.residual_mix_bwd_ckpt(Xq, H, h, Fq, Y, need_dlogits=True)
+    one = api.residual_mix_bwd_ckpt(Xq1, cut[1], cut[2], Fq1, Y1, need_dlogits=True)
+    assert all(torch.equal(out[k][-n:], one[k]) for k in out)
+    del out, Y
+    torch.cuda.empty_cache()
+    dF, dh = api.mix_post_bwd_ckpt(X, Fq, h)
+    assert _tail_equals((dF, dh), api.mix_post_bwd_ckpt(cut[0], Fq1, cut[2]), n)
+    out = api.mix_premap_bwd_ckpt(Xq, H, h, X, F)
+    one = api.mix_premap_bwd_ckpt(Xq1, cut[1], cut[2], cut[0], cut[3])
+    assert torch.equal(out["dX"][-n:], one["dX"]) and torch.equal(out["dh_pre"][-n:], one["dh_pre"])
+    del out, dF, Xq, Fq
+    torch.cuda.empty_cache()
+    a = api.premap_fwd_mx4(X, h)
+    assert _tail_equals(a[:2], api.premap_fwd_mx4(cut[0], cut[2])[:2], n)
+    # the product's forms sum in different orders: compared within two roundings of its terms
+    a = api.mx_pack(torch.randn((T, 64), generator=g, device=d, dtype=torch.bfloat16), "e2m1")
+    w = api.mx_pack(torch.randn((C * 4, 64), generator=g, device=d, dtype=torch.bfloat16), "e2m1")
+    part = api.MxTensor(a.codes[-n:].clone(), a.scales[-n:].clone(), "e2m1")
+    big, small = api.mx4_linear(a, w)[-n:].float(), api.mx4_linear(part, w).float()
+    assert ((big - small).abs() <= 2 * BF16 * small.abs() + 1e-4).all()
+    w = api.MxTensor(w.codes[:C].clone(), w.scales[:C].clone(), "e2m1")
+    Z = api.mx4_linear_mix(a, w, X, H, h)[-n:].float()
+    Z1 = api.mx4_linear_mix(part, w, cut[0], cut[1], cut[2]).float()
+    assert ((Z - Z1).abs() <= 2 * BF16 * Z1.abs() + 1e-4).all()
+    api.wait_status()
+    del X, F, Z, big, a
+    torch.cuda.empty_cache()
