@@ -86,7 +86,13 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 // cycles a K tile, and so, 290.)  A pair loads 28 KB a K tile and CTA where
 // single CTAs load 40.
 //
-// MEASURED
+// Measured (device, back to back, operands not in L2 for few tokens): 8192
+// tokens, N = 8192, K = 4096 109 us, 5.0 PFLOP/s (the instruction's own rate
+// would be 65 us; the scales' loads cost 12 of the rest, the output 20); 200
+// tokens, N = 4104, K = 4096 9.3 us; one token, N = 8192, K = 7168 9.7 us
+// (3.2 TB/s, latency: the launch, the first bytes of memory and the cluster's
+// sum).  With the mix: 16384 tokens, C = 4096, K = 8192 321 us, of which the
+// streams' loads and Y's stores are about 40 each.
 //
 // Every wait is bounded (tc5.cuh).  One that runs out, which no valid call
 // does, sets mx4_wait_expired, makes the other roles give up too, and leaves
@@ -145,14 +151,14 @@ struct ProductShape {
 // The scales of 512 elements of one row, and of the next 512 if `two`: 16 bytes
 // each, in as few loads as the rows' alignment (32, 16 or 4 bytes) allows,
 // since every lane reads another row and each load costs a pass over 32 cache
-// lines.  Words past the row read as zero.  Volatile, so that the loads stay
+// lines (which the 32-byte form, done with its sector, does not keep).  Words past the row read as zero.  Volatile, so that the loads stay
 // where they are issued, a round ahead of their use.
 __device__ __forceinline__ void fetch_scales(const uint8_t* row, int pair, bool two, int pitch, int align, uint4& q0,
                                              uint4& q1)
 {
     const uint8_t* at = row + 16 * pair;
     if (align == 32 && two) {
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(q0.x), "=r"(q0.y), "=r"(q0.z), "=r"(q0.w), "=r"(q1.x), "=r"(q1.y), "=r"(q1.z), "=r"(q1.w)
                      : "l"(at));
     } else if (align >= 16) {
@@ -683,7 +689,7 @@ using Pair192 = ProductShape<192, kMix ? 4 : 5, true>;
 // while their tiles fit the GPU at once, and the narrowest that holds the
 // tokens: at N = 8192, K = 4096 one token takes 7.9 us in tiles of 16 and
 // 9.2 in tiles of 64; 200 tokens take 17.6 us in tiles of 64 (256 tiles, two
-// waves) and PAIR200 in pairs.
+// waves) and 13.4 in pairs.
 template <bool kMix>
 cudaError_t product_by_size(const uint8_t* A, const uint8_t* W, const ProductArgs& p, cudaStream_t s)
 {
