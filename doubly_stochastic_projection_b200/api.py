@@ -509,14 +509,12 @@ def _mx_format(fmt, allowed=("int8", "e4m3", "e2m1")):
 
 def _mx_empty(like, shape, fmt):
     """An unwritten MxTensor of `shape` beside a tensor."""
-    C = shape[-1]
-    if fmt == "e2m1":
-        codes = like.new_empty((*shape[:-1], C // 2), dtype=torch.uint8)
-    elif like.shape == shape:
+    *rows, C = shape
+    if fmt != "e2m1" and like.shape == shape:
         codes = torch.empty_like(like, dtype=torch.uint8)
     else:
-        codes = like.new_empty(shape, dtype=torch.uint8)
-    return MxTensor(codes, like.new_empty((*shape[:-1], 4 * ((C + 127) // 128)), dtype=torch.uint8), fmt)
+        codes = like.new_empty((*rows, C // 2 if fmt == "e2m1" else C), dtype=torch.uint8)
+    return MxTensor(codes, codes.new_empty((*rows, 4 * ((C + 127) // 128))), fmt)
 
 
 def _need_mx(mx, name, allowed, shape=None):
@@ -526,14 +524,15 @@ def _need_mx(mx, name, allowed, shape=None):
     codes, scales, fmt = mx
     if fmt not in allowed:
         _mx_format(fmt, allowed)
-    s = tuple(_need(codes, name, torch.uint8).shape)
-    if not s:
+    *rows, C = _need(codes, name, torch.uint8).shape or (None,)
+    if C is None:
         raise ValueError("%s.codes must have at least one dimension" % name)
     if fmt == "e2m1":
-        s = (*s[:-1], 2 * s[-1])
+        C *= 2
+    _need(scales, name, torch.uint8, (*rows, 4 * ((C + 127) // 128)))
+    s = (*rows, C)
     if shape is not None and s != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), s))
-    _need(scales, name, torch.uint8, (*s[:-1], 4 * ((s[-1] + 127) // 128)))
     return s
 
 
@@ -545,24 +544,21 @@ def _launch(f, tensors, *numbers):
     the numbers, on the current stream of the tensors' device: they must share
     one, which is made current for the launch if it is not."""
     dev = tensors[0].get_device()
-    ptrs = []
-    for t in tensors:
-        if t is None:
-            ptrs.append(None)
-        elif t.get_device() == dev:
-            ptrs.append(t.data_ptr())
-        else:
-            raise ValueError("tensors are on %s and %s" % (tensors[0].device, t.device))
+    ptrs = [t if t is None else t.data_ptr() if t.get_device() == dev else _other_device(tensors) for t in tensors]
     # the handle behind torch.cuda.current_stream(dev).cuda_stream, without the
     # Stream object: small calls are bound by this thread
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         rc = f(*ptrs, *numbers, stream)
     else:
         with torch.cuda.device(dev):
             rc = f(*ptrs, *numbers, stream)
-    if rc != 0:
+    if rc:
         _check(rc)
+
+
+def _other_device(tensors):
+    raise ValueError("tensors are on several devices: %s" % ", ".join(str(t.device) for t in tensors if t is not None))
 
 
 def mx_pack(x, fmt, out: MxTensor | None = None) -> MxTensor:
@@ -580,7 +576,7 @@ def mx_pack(x, fmt, out: MxTensor | None = None) -> MxTensor:
         out = _mx_empty(x, shape, fmt)
     else:
         _need_mx(out, "out", (fmt,), shape)
-    _launch(lib().mhc_mx_pack, (x, out.codes, out.scales), x.numel() // C if C else 0, C, f)
+    _launch(lib().mhc_mx_pack, (x, out[0], out[1]), x.numel() // C if C else 0, C, f)
     return out
 
 
@@ -592,7 +588,7 @@ def mx_unpack(mx: MxTensor, out=None):
         out = mx.codes.new_empty(shape, dtype=torch.bfloat16)
     else:
         _need(out, "out", torch.bfloat16, shape)
-    _launch(lib().mhc_mx_unpack, (mx.codes, mx.scales, out), out.numel() // C if C else 0, C, _MX_FORMATS[mx.fmt])
+    _launch(lib().mhc_mx_unpack, (mx[0], mx[1], out), out.numel() // C if C else 0, C, _MX_FORMATS[mx.fmt])
     return out
 
 
@@ -605,7 +601,7 @@ def residual_mix_fwd_ckpt(X, H_res, h_post, F, fmt="int8", out=None):
     _need(h_post, "h_post", torch.float32, (T, 4))
     Y = torch.empty_like(X) if out is None else _need(out, "out", torch.bfloat16, X.shape)
     Xq, Fq = _mx_empty(X, (T, 4, C), fmt), _mx_empty(F, (T, C), fmt)
-    _launch(lib().mhc_residual_mix_fwd_ckpt, (X, H_res, h_post, F, Y, *Xq[:2], *Fq[:2]), T, C, f)
+    _launch(lib().mhc_residual_mix_fwd_ckpt, (X, H_res, h_post, F, Y, Xq[0], Xq[1], Fq[0], Fq[1]), T, C, f)
     return Y, Xq, Fq
 
 
@@ -619,7 +615,7 @@ def proj_mix_fwd_ckpt(logits, h_post, X, F, fmt="int8", iters: int = 0, out=None
     Y = torch.empty_like(X) if out is None else _need(out, "out", torch.bfloat16, X.shape)
     H = torch.empty_like(logits)
     Xq, Fq = _mx_empty(X, (T, 4, C), fmt), _mx_empty(F, (T, C), fmt)
-    _launch(lib().mhc_proj_mix_fwd_ckpt, (logits, h_post, X, F, Y, H, *Xq[:2], *Fq[:2]), T, C, int(iters), f)
+    _launch(lib().mhc_proj_mix_fwd_ckpt, (logits, h_post, X, F, Y, H, Xq[0], Xq[1], Fq[0], Fq[1]), T, C, int(iters), f)
     return Y, H, Xq, Fq
 
 
@@ -651,7 +647,7 @@ def residual_mix_bwd_ckpt(Xq: MxTensor, H_res, h_post, Fq: MxTensor, dY, need_dH
     dH = torch.empty_like(H_res) if need_dH else None
     dh = torch.empty_like(h_post) if need_dh_post else None
     dl = torch.empty_like(H_res) if need_dlogits else None
-    _launch(lib().mhc_residual_mix_bwd_ckpt, (*Xq[:2], H_res, h_post, *Fq[:2], dY, dX, dH, dh, dF, dl), T, C,
+    _launch(lib().mhc_residual_mix_bwd_ckpt, (Xq[0], Xq[1], H_res, h_post, Fq[0], Fq[1], dY, dX, dH, dh, dF, dl), T, C,
             _MX_FORMATS[Xq.fmt])
     return {"dX": dX, "dF": dF, "dH_res": dH, "dh_post": dh, "dlogits": dl}
 
@@ -670,7 +666,7 @@ def mix_post_bwd_ckpt(dY, Fq: MxTensor, h_post):
     _need(h_post, "h_post", torch.float32, (T, 4))
     dF = dY.new_empty((T, C))
     dh = torch.empty_like(h_post)
-    _launch(lib().mhc_mix_post_bwd_ckpt, (dY, *Fq[:2], h_post, dF, dh), T, C, _MX_FORMATS[Fq.fmt])
+    _launch(lib().mhc_mix_post_bwd_ckpt, (dY, Fq[0], Fq[1], h_post, dF, dh), T, C, _MX_FORMATS[Fq.fmt])
     return dF, dh
 
 
@@ -686,7 +682,7 @@ def mix_premap_bwd_ckpt(Xq: MxTensor, H_res, h_pre, dY, dx_in, need_dH=False, ne
     dhp = torch.empty_like(h_pre)
     dH = torch.empty_like(H_res) if need_dH else None
     dl = torch.empty_like(H_res) if need_dlogits else None
-    _launch(lib().mhc_mix_premap_bwd_ckpt, (*Xq[:2], H_res, h_pre, dY, dx_in, dX, dH, dhp, dl), T, C,
+    _launch(lib().mhc_mix_premap_bwd_ckpt, (Xq[0], Xq[1], H_res, h_pre, dY, dx_in, dX, dH, dhp, dl), T, C,
             _MX_FORMATS[Xq.fmt])
     return {"dX": dX, "dh_pre": dhp, "dH_res": dH, "dlogits": dl}
 
@@ -698,7 +694,7 @@ def premap_fwd_mx4(X, h_pre) -> MxTensor:
     T, C = _streams_shape(X, "X")
     _need(h_pre, "h_pre", torch.float32, (T, 4))
     out = _mx_empty(X, (T, C), "e2m1")
-    _launch(lib().mhc_premap_fwd_mx4, (X, h_pre, *out[:2]), T, C)
+    _launch(lib().mhc_premap_fwd_mx4, (X, h_pre, out[0], out[1]), T, C)
     return out
 
 
@@ -718,7 +714,7 @@ def mx4_linear(a: MxTensor, w: MxTensor, out=None):
         out = a.codes.new_empty((T, N), dtype=torch.bfloat16)
     else:
         _need(out, "out", torch.bfloat16, (T, N))
-    _launch(lib().mhc_mx4_linear, (*a[:2], *w[:2], out), T, N, K)
+    _launch(lib().mhc_mx4_linear, (a[0], a[1], w[0], w[1], out), T, N, K)
     return out
 
 
@@ -733,7 +729,7 @@ def mx4_linear_mix(a: MxTensor, w: MxTensor, X, H_res, h_post, out=None):
         out = torch.empty_like(X)
     else:
         _need(out, "out", torch.bfloat16, X.shape)
-    _launch(lib().mhc_mx4_linear_mix, (*a[:2], *w[:2], X, H_res, h_post, out), T, C, K)
+    _launch(lib().mhc_mx4_linear_mix, (a[0], a[1], w[0], w[1], X, H_res, h_post, out), T, C, K)
     return out
 
 
