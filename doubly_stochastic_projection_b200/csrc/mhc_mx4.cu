@@ -91,7 +91,7 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 // would be 65 us; the scales' loads cost 12 of the rest, the output 20); 200
 // tokens, N = 4104, K = 4096 9.3 us; one token, N = 8192, K = 7168 9.7 us
 // (3.2 TB/s, latency: the launch, the first bytes of memory and the cluster's
-// sum).  With the mix: 16384 tokens, C = 4096, K = 8192 321 us, of which the
+// sum).  With the mix: 16384 tokens, C = 4096, K = 8192 311 us, of which the
 // streams' loads and Y's stores are about 40 each.
 //
 // Every wait is bounded (tc5.cuh).  One that runs out, which no valid call
@@ -151,8 +151,9 @@ struct ProductShape {
 // The scales of 512 elements of one row, and of the next 512 if `two`: 16 bytes
 // each, in as few loads as the rows' alignment (32, 16 or 4 bytes) allows,
 // since every lane reads another row and each load costs a pass over 32 cache
-// lines (which the 32-byte form, done with its sector, does not keep).  Words past the row read as zero.  Volatile, so that the loads stay
-// where they are issued, a round ahead of their use.
+// lines (which the 32-byte form, done with its sector, does not keep).  Words past
+// the row read as zero.  Volatile, so that the loads stay where they are issued, a
+// round ahead of their use.
 __device__ __forceinline__ void fetch_scales(const uint8_t* row, int pair, bool two, int pitch, int align, uint4& q0,
                                              uint4& q1)
 {
@@ -192,6 +193,29 @@ __device__ __forceinline__ uint32_t scales_within(uint32_t word, int w, int KB)
 
 // What the output of eight channels of a token (vector v of N / 8) takes beside
 // the product: nothing, or the mix's streams and maps, loaded ahead.
+// Two floats in one register pair.  The mix's 160 multiply-adds for a token and
+// vector, two channels an instruction: each rounds as fmaf does, and 16384 x
+// 4096 x 8192 takes 311 us instead of 321, the epilogue's eight warps being
+// bound by what they issue.
+__device__ __forceinline__ uint64_t two(float lo, float hi)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 template <bool kMix>
 struct StreamVec {
     __device__ __forceinline__ void load(const ProductArgs&, int64_t, int) {}
@@ -214,18 +238,26 @@ struct StreamVec<true> {
     __device__ __forceinline__ void emit(const ProductArgs& p, const float (&f)[8], int64_t t, int v) const
     {
         const int NV = p.N >> 3;
-        float xf[4][8];
+        uint64_t xf[4][4], ff[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) unpack8(x[j], xf[j]);
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) xf[j][e] = two(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ff[e] = two(f[2 * e], f[2 * e + 1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float o[8];
+            const uint64_t hh[5] = {two(hp[i], hp[i]), two(h[4 * i], h[4 * i]), two(h[4 * i + 1], h[4 * i + 1]),
+                                    two(h[4 * i + 2], h[4 * i + 2]), two(h[4 * i + 3], h[4 * i + 3])};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float s = hp[i] * f[e];
+            for (int e = 0; e < 4; ++e) {
+                uint64_t s = mul2(hh[0], ff[e]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s = fmaf(h[4 * i + j], xf[j][e], s);
-                o[e] = s;
+                for (int j = 0; j < 4; ++j) s = fma2(hh[1 + j], xf[j][e], s);
+                asm("mov.b64 {%0, %1}, %2;" : "=f"(o[2 * e]), "=f"(o[2 * e + 1]) : "l"(s));
             }
             __stcs(p.out + (t * 4 + i) * NV + v, pack8(o));
         }
