@@ -91,8 +91,8 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 // would be 65 us; the scales' loads cost 12 of the rest, the output 20); 200
 // tokens, N = 4104, K = 4096 9.3 us; one token, N = 8192, K = 7168 9.7 us
 // (3.2 TB/s, latency: the launch, the first bytes of memory and the cluster's
-// sum).  With the mix: 16384 tokens, C = 4096, K = 8192 311 us, of which the
-// streams' loads and Y's stores are about 40 each.
+// sum).  With the mix: 16384 tokens, C = 4096, K = 8192 311 to 321 us by
+// the GPU, of which the streams' loads and Y's stores are about 40 each.
 //
 // Every wait is bounded (tc5.cuh).  One that runs out, which no valid call
 // does, sets mx4_wait_expired, makes the other roles give up too, and leaves
@@ -195,8 +195,8 @@ __device__ __forceinline__ uint32_t scales_within(uint32_t word, int w, int KB)
 // the product: nothing, or the mix's streams and maps, loaded ahead.
 // Two floats in one register pair.  The mix's 160 multiply-adds for a token and
 // vector, two channels an instruction: each rounds as fmaf does, and 16384 x
-// 4096 x 8192 takes 311 us instead of 321, the epilogue's eight warps being
-// bound by what they issue.
+// 4096 x 8192 takes 321 us instead of 327 timed in turn, 1000 tokens 40 instead of
+// 42, the epilogue's eight warps being bound by what they issue.
 __device__ __forceinline__ uint64_t two(float lo, float hi)
 {
     uint64_t d;
