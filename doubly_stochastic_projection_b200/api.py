@@ -581,7 +581,8 @@ def mx_pack(x, fmt, out: MxTensor | None = None) -> MxTensor:
 
 
 def mx_unpack(mx: MxTensor, out=None):
-    """The bf16 tensor that a microscaled tensor stands for (exact in bf16)."""
+    """The bf16 tensor that a microscaled tensor stands for: exact, but for values
+    next to 2^128, which round to infinity."""
     shape = _need_mx(mx, "mx", tuple(_MX_FORMATS))
     C = shape[-1]
     if out is None:
