@@ -20,6 +20,7 @@
 #include "launch.h"
 #include "mix_common.cuh"
 #include "mx_common.cuh"
+#include "pdl.cuh"
 
 namespace mhc {
 
@@ -164,6 +165,7 @@ template <int kFmt, bool kWide>
 __global__ void __launch_bounds__(kPackThreads)
 mx_pack_kernel(const uint4* x, uint8_t* codes, uint8_t* scales, int64_t R, int CV)
 {
+    if (kFmt == MHC_MX_E2M1) pdl_release();  // the product's operand
     BlockWalk w(R, CV);
     // a warp goes on while any of its lanes has blocks: all take part in the shuffles
     while (__any_sync(0xffffffffu, !w.done())) {

@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(kReadThreads)
 premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t* scales, int64_t T, int chunks, int CV)
 {
     const int64_t sp = mx_scale_pitch((int64_t)CV * 8);
+    pdl_release();  // the product waits for this kernel's end by itself
     const unsigned dt = gridDim.x / chunks, dk = gridDim.x % chunks;
     unsigned k = blockIdx.x % chunks;
     int64_t t = blockIdx.x / chunks;

@@ -481,6 +481,49 @@ def test_side_streams_and_graph_replay():
     del g
 
 
+@pytest.mark.parametrize("T", (1, 16, 200, 2500))
+def test_product_follows_its_operands(T):
+    # one operand's buffers, written anew for each product while the last may still run
+    N = K = 1024
+    w = api.mx_pack(streams((N, K), 71, outliers=False), "e2m1")
+    xs = [streams((T, K), 72 + i, outliers=False) for i in range(4)]
+    h_pre = to_gpu(np.random.default_rng(73).standard_normal((T, 4)).astype(np.float32))
+    ref = []
+    for x in xs:
+        a = api.mx_pack(x, "e2m1")
+        torch.cuda.synchronize()
+        u = api.mx4_linear(a, w)
+        torch.cuda.synchronize()
+        b = api.premap_fwd_mx4(torch.stack([u, x, u, x], 1), h_pre)
+        torch.cuda.synchronize()
+        ref.append(api.mx4_linear(b, w))
+        torch.cuda.synchronize()
+    a = api.mx_pack(xs[0], "e2m1")
+    X = torch.empty((T, 4, K), dtype=torch.bfloat16, device=dev())
+    u = torch.empty((T, N), dtype=torch.bfloat16, device=dev())
+
+    def chain():
+        got = []
+        for x in xs:
+            api.mx_pack(x, "e2m1", out=a)
+            api.mx4_linear(a, w, out=u)
+            for j in range(4):
+                X[:, j].copy_(x if j & 1 else u)
+            got.append(api.mx4_linear(api.premap_fwd_mx4(X, h_pre), w))
+        return got
+
+    for _ in range(20):
+        assert all(torch.equal(g, r) for g, r in zip(chain(), ref))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain()
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, r) for g, r in zip(out, ref))
+    del graph
+
+
 def test_empty_batches():
     d = dev()
     for fmt in FORMATS:
