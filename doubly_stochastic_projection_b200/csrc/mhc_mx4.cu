@@ -89,26 +89,24 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 //         of four rows, a round ahead, and stores 16-byte vectors
 //   4-11  the epilogue: tensor memory -> shared memory, turned so that a
 //         thread holds eight consecutive channels of a token -> the output
-// Two forms.  Split: a cluster shares one output tile, each CTA a part of K; the
-// partial sums meet in shared memory and are added in the order of the ranks.
-// Pair: persistent pairs of CTAs walk output tiles of 256 channels, each CTA
-// with its 128 rows of W, half of the tile's tokens as operand and the sums of
-// its rows; the sums of one tile are in one half of tensor memory while the
-// epilogue drains the other.  The CTA of rank 0 issues the tensor instructions
-// for both.  It hears that the other's operands are there from that CTA's warps
-// 1 and 2, which wait for their own barriers and pass each on by an empty
-// commit: one message a K tile.  (TMA loads that count their bytes at the
-// other CTA's barrier send one a row or so; the loads alone then took 600
-// cycles a K tile, and so, 290.)  A pair loads 28 KB a K tile and CTA where
-// single CTAs load 40.
+// Two forms.  Whole: one persistent CTA an SM walks output tiles, the sums of
+// one tile in one half of tensor memory while the epilogue drains the other.
+// Split: a cluster shares one output tile, each CTA a part of K; the partial
+// sums meet in shared memory and are added in the order of the ranks.
+// No form has operands in two CTAs.  Pairs of CTAs on one tile (256 channels,
+// 28 KB a K tile and CTA instead of 40) need word, for each K tile, that the
+// other's operands are there.  Given by an arrival that releases at cluster scope
+// a K tile took 1400 cycles, of which the products need 384 (8192 tokens, N =
+// 8192, K = 4096 229 us); given by TMA loads that count their bytes at the other
+// CTA's barrier, 600 (175 us).  A commit without tensor work before it is quick,
+// but nothing says that it orders what its thread has waited for.
 //
 // Measured (device, back to back, operands not in L2 for few tokens): 8192
-// tokens, N = 8192, K = 4096 109 us, 5.0 PFLOP/s (the instruction's own rate
-// would be 65 us; the scales' loads cost 12 of the rest, the output 20); 200
-// tokens, N = 4104, K = 4096 9.3 us; one token, N = 8192, K = 7168 9.7 us
-// (3.2 TB/s, latency: the launch, the first bytes of memory and the cluster's
-// sum).  With the mix: 16384 tokens, C = 4096, K = 8192 311 to 321 us by
-// the GPU, of which the streams' loads and Y's stores are about 40 each.
+// tokens, N = 8192, K = 4096 115 us, 4.8 PFLOP/s (the instruction's own rate
+// would be 65 us; operands, scales and outputs share the path between L2 and the
+// SMs); 200 tokens, N = 4104, K = 4096 9.3 us; one token, N = 8192, K = 7168
+// 9.8 us (3.2 TB/s, latency: the launch, the first bytes of memory and the
+// cluster's sum).  With the mix: 16384 tokens, C = 4096, K = 8192 322 to 325 us.
 //
 // Every wait is bounded (tc5.cuh).  One that runs out, which no valid call
 // does, sets mx4_wait_expired, makes the other roles give up too, and leaves
@@ -133,15 +131,13 @@ struct ProductArgs {
     int chan_tiles, tok_tiles;
 };
 
-template <int kTok_, int kStages_, bool kPair_>
+template <int kTok_, int kStages_, bool kSplit_>
 struct ProductShape {
     static constexpr int kTok = kTok_, kStages = kStages_;
-    static constexpr bool kPair = kPair_, kSplit = !kPair;
-    static constexpr int kTileChan = kPair ? 2 * kChan : kChan;  // channels of an output tile
-    static constexpr int kTokRows = kPair ? kTok / 2 : kTok;     // of A that a CTA loads
+    static constexpr bool kSplit = kSplit_;
     static constexpr int kTokChunks = (kTok + 127) / 128;  // 128-row chunks of A's scales
     static constexpr int kThreads = 32 * (12 + kTokChunks);  // four warps a scheduler: 128 registers at most
-    static constexpr int kWBytes = kChan * kRowBytes, kABytes = kTokRows * kRowBytes;
+    static constexpr int kWBytes = kChan * kRowBytes, kABytes = kTok * kRowBytes;
     static constexpr int kStageBytes = kWBytes + kABytes;
     // scales: two buffers of kBufTiles K tiles, each tile two steps of 128
     // elements, a step's being one chunk of W's and kTokChunks of A's
@@ -308,44 +304,36 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
     // operands of the tensor instructions then stay in uniform registers, and the
     // four steps of a K tile issue in about 220 cycles instead of 280.
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int rank = __shfl_sync(0xffffffffu, (int)tc5::cluster_rank(), 0);
-    constexpr bool kPair = S::kPair;
-    const bool leads = !kPair || rank == 0;  // issues the tensor instructions
     if (warp == 0 && lane == 0) {
         tc5::prefetch_map(&mapW);
         tc5::prefetch_map(&mapA);
         for (int s = 0; s < kStages; ++s) {
-            // the codes by TMA; where products are issued also the scales by tensor
-            // copy, and word that the other CTA's codes are there
-            tc5::mbar_init(full(s), 1 + (leads ? 1 : 0) + (kPair && leads ? 1 : 0));
+            tc5::mbar_init(full(s), 2);  // the codes by TMA, the scales by tensor copy
             tc5::mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
-            tc5::mbar_init(scales_full(b), 1 + S::kTokChunks + (kPair && leads ? 1 : 0));  // the scale warps; the same
+            tc5::mbar_init(scales_full(b), 1 + S::kTokChunks);  // the scale warps
             tc5::mbar_init(scales_empty(b), 1);
         }
         for (int a = 0; a < S::kSums; ++a) {
             tc5::mbar_init(sum_full(a), 1);
-            tc5::mbar_init(sum_empty(a), kEpiWarps * (kPair ? 2 : 1));
+            tc5::mbar_init(sum_empty(a), kEpiWarps);
         }
         tc5::mbar_init(drained, 2);
         *abort = 0;
         tc5::fence_mbar_init();
     }
-    if (warp == 1) tc5::tmem_alloc<S::kColumns, kPair>(tc5::smem_addr(tmem_slot));
+    if (warp == 1) tc5::tmem_alloc<S::kColumns>(tc5::smem_addr(tmem_slot));
     tc5::fence_before_sync();
     __syncthreads();
-    if (kPair) tc5::cluster_sync();  // the other CTA's barriers and tensor memory are there
     tc5::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     pdl_wait();
 
-    // this cluster's output tiles; this CTA's share of K, in pairs of tiles, or of
-    // the tile's channels
-    const int ranks = (int)tc5::cluster_size();
+    // this CTA's output tiles, and its share of K in pairs of tiles
+    const int ranks = S::kSplit ? (int)tc5::cluster_size() : 1, rank = S::kSplit ? (int)tc5::cluster_rank() : 0;
     const int pairs = (p.K + 511) / 512;  // 16 bytes of scales
-    const int pair0 = kPair ? 0 : pairs * rank / ranks, pair1 = kPair ? pairs : pairs * (rank + 1) / ranks;
-    const int my_chan = kPair ? rank * kChan : 0;
+    const int pair0 = pairs * rank / ranks, pair1 = pairs * (rank + 1) / ranks;
     const int k0 = 2 * pair0, k1 = min(2 * pair1, (p.K + 255) / 256);
     const int tiles = p.chan_tiles * p.tok_tiles;
     const int first = blockIdx.x / ranks, stride = gridDim.x / ranks;
@@ -357,8 +345,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         uint32_t phase = 0;
         int64_t loads = 0;
         for (int n = 0; n < mine && ok; ++n, t += stride) {
-            const int n0 = t % p.chan_tiles * S::kTileChan + my_chan;
-            const int t0 = t / p.chan_tiles * kTok + (kPair ? rank * S::kTokRows : 0);
+            const int n0 = t % p.chan_tiles * kChan, t0 = t / p.chan_tiles * kTok;
             for (int k = k0; k < k1; ++k, ++loads) {
                 if (!(ok = tc5::mbar_wait_warp(empty(s), phase ^ 1, abort))) break;
                 const uint32_t at = base + s * S::kStageBytes;
@@ -377,22 +364,6 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
             for (int64_t j = loads > kStages ? loads - kStages : 0; j < loads; ++j)
                 tc5::mbar_wait(full((int)(j % kStages)), (uint32_t)(j / kStages) & 1, nullptr, kDrainNs);
         }
-    } else if (!leads && (warp == 1 || warp == 2)) {
-        // word to the other CTA: this one's codes (warp 1) or scales (warp 2) are there
-        const int slots = warp == 1 ? kStages : 2, every = warp == 1 ? 1 : S::kBufTiles;
-        const uint32_t bar0 = warp == 1 ? full(0) : scales_full(0);
-        int s = 0;
-        uint32_t phase = 0;
-        for (int n = 0; n < mine && ok; ++n) {
-            for (int k = 0; k < steps; k += every) {
-                if (!(ok = tc5::mbar_wait_warp(bar0 + 8 * s, phase, abort))) break;
-                if (tc5::elect_one()) tc5::commit<kPair>(tc5::map_rank(bar0 + 8 * s, 0));
-                __syncwarp();
-                s = s + 1 == slots ? 0 : s + 1;
-                phase ^= s == 0;
-            }
-        }
-        if (!ok) *abort = 1;
     } else if (warp == 2) {
         // each K tile's scales from shared into tensor memory, ahead of the products
         int s = 0, buf = 0;
@@ -400,7 +371,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         for (int n = 0; n < mine && ok; ++n) {
             for (int k = 0; k < steps; ++k) {
                 const int j = k & (S::kBufTiles - 1);  // in this buffer
-                if (j == 0 && !(ok = tc5::mbar_wait_warp<kPair>(scales_full(buf), par, abort))) break;
+                if (j == 0 && !(ok = tc5::mbar_wait_warp(scales_full(buf), par, abort))) break;
                 if (!(ok = tc5::mbar_wait_warp(empty(s), phase ^ 1, abort))) break;
                 tc5::fence_after_sync();
                 const uint32_t at = base + kOffScales + (buf * S::kBufSteps + 2 * j) * S::kScaleStep;
@@ -409,9 +380,9 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 if (tc5::elect_one()) {
 #pragma unroll
                     for (int c = 0; c < 2 * (1 + S::kTokChunks); ++c)
-                        tc5::copy_scales<kPair>(sw + 4 * c, tc5::scale_desc(at + 512 * c));
-                    tc5::commit<kPair>(full(s));
-                    if (last) tc5::commit_both<kPair>(scales_empty(buf));
+                        tc5::copy_scales(sw + 4 * c, tc5::scale_desc(at + 512 * c));
+                    tc5::commit(full(s));
+                    if (last) tc5::commit(scales_empty(buf));
                 }
                 __syncwarp();
                 s = s + 1 == kStages ? 0 : s + 1;
@@ -422,7 +393,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         }
         if (!ok) {
             *abort = 1;
-            if (tc5::elect_one()) tc5::commit<kPair>(drained);
+            if (tc5::elect_one()) tc5::commit(drained);
             __syncwarp();
             tc5::mbar_wait(drained, 0, nullptr, kDrainNs);
         }
@@ -430,13 +401,13 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         // The whole warp waits, one lane issues.  The queue behind it is short
         // (a delay of some 150 cycles between two K tiles is hidden, one of 250 is
         // not), so nothing else is done here.
-        constexpr uint32_t inst = tc5::mx4_instruction(S::kTileChan, kTok);
+        constexpr uint32_t inst = tc5::mx4_instruction(kChan, kTok);
         int s = 0;
         uint32_t phase = 0;
-        if (mine > 0) ok = tc5::mbar_wait_warp<kPair>(full(0), 0, abort);
+        if (mine > 0) ok = tc5::mbar_wait_warp(full(0), 0, abort);
         for (int n = 0; n < mine && ok; ++n) {
             const int a = n % S::kSums;
-            if (!(ok = tc5::mbar_wait_warp<kPair>(sum_empty(a), (n / S::kSums & 1) ^ 1, abort))) break;
+            if (!(ok = tc5::mbar_wait_warp(sum_empty(a), (n / S::kSums & 1) ^ 1, abort))) break;
             const uint32_t d = tmem + a * kTok;
             for (int k = 0; k < steps; ++k) {
                 tc5::fence_after_sync();
@@ -449,8 +420,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 // 64 elements a step, 32 bytes along the swizzled row
                 const auto step = [&](int q) {
                     const uint32_t sw = sc + 4 * (1 + S::kTokChunks) * (q >> 1);
-                    tc5::mma_mx4<kPair>(d, dw + 2 * q, da + 2 * q, inst | tc5::scale_select(2 * (q & 1)), sw, sw + 4,
-                                        k > 0 || q > 0);
+                    tc5::mma_mx4(d, dw + 2 * q, da + 2 * q, inst | tc5::scale_select(2 * (q & 1)), sw, sw + 4,
+                                 k > 0 || q > 0);
                 };
                 if (tc5::elect_one()) {
                     step(0);
@@ -459,11 +430,11 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 }
                 __syncwarp();
                 // the next K tile's wait, while the queue holds steps of this one
-                if (k + 1 < steps || n + 1 < mine) ok = tc5::mbar_wait_warp<kPair>(full(s), phase, abort);
+                if (k + 1 < steps || n + 1 < mine) ok = tc5::mbar_wait_warp(full(s), phase, abort);
                 if (tc5::elect_one()) {
                     step(3);
-                    tc5::commit_both<kPair>(empty(here));
-                    if (k + 1 == steps) tc5::commit_both<kPair>(sum_full(a));
+                    tc5::commit(empty(here));
+                    if (k + 1 == steps) tc5::commit(sum_full(a));
                 }
                 __syncwarp();
                 if (!ok) break;
@@ -471,7 +442,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         }
         if (!ok) {
             *abort = 1;  // the tensor work in flight, before its memory is freed
-            if (tc5::elect_one()) tc5::commit<kPair>(drained);
+            if (tc5::elect_one()) tc5::commit(drained);
             __syncwarp();
             tc5::mbar_wait(drained, 0, nullptr, kDrainNs);
         }
@@ -491,8 +462,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         uint4 cur[2][4], next[2][4];
         const auto fetch = [&](int tile, int pair) {
             if (tile >= tiles) return;
-            const int64_t r0 = isW ? (int64_t)(tile % p.chan_tiles) * S::kTileChan + my_chan
-                                   : (int64_t)(tile / p.chan_tiles) * kTok + in_tile;
+            const int64_t r0 =
+                isW ? (int64_t)(tile % p.chan_tiles) * kChan : (int64_t)(tile / p.chan_tiles) * kTok + in_tile;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 // rows past the end, or past the tile, stand in for none: what they
@@ -544,7 +515,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         int n = 0;
         for (int tile = first; tile < tiles; tile += stride, ++n) {
             const int a = n % S::kSums;
-            const int v0 = (tile % p.chan_tiles * S::kTileChan + my_chan) / 8;
+            const int v0 = tile % p.chan_tiles * (kChan / 8);
             const int64_t t0 = (int64_t)(tile / p.chan_tiles) * kTok;
             if (ok) ok = tc5::mbar_wait_warp(sum_full(a), n / S::kSums & 1, abort);
             tc5::fence_after_sync();
@@ -576,12 +547,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                     if (g + S::kGroup >= kTok) {  // the last read of this tile's sums
                         tc5::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) {
-                            if (leads)
-                                tc5::mbar_arrive(sum_empty(a));
-                            else
-                                tc5::mbar_arrive_cluster(tc5::map_rank(sum_empty(a), 0));
-                        }
+                        if (lane == 0) tc5::mbar_arrive(sum_empty(a));
                     }
                     // two buffers in turn: by the barrier of the next group, all have read this one
                     float* buf = epi + (g & S::kGroup) * kChan;
@@ -631,10 +597,9 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
     }
     tc5::fence_before_sync();
     __syncthreads();
-    if (kPair) tc5::cluster_sync();  // both are done with each other's memory and barriers
     if (warp == 1) {
         tc5::fence_after_sync();
-        tc5::tmem_free<S::kColumns, kPair>(tmem);
+        tc5::tmem_free<S::kColumns>(tmem);
     }
 }
 
@@ -697,20 +662,19 @@ cudaError_t product(const uint8_t* A, const uint8_t* W, ProductArgs p, cudaStrea
         if (e != cudaSuccess) return e;
         if (dev < 64) allowed.fetch_or(uint64_t(1) << dev, std::memory_order_release);
     }
-    p.chan_tiles = (p.N + S::kTileChan - 1) / S::kTileChan;
+    p.chan_tiles = (p.N + kChan - 1) / kChan;
     p.tok_tiles = (int)((p.T + S::kTok - 1) / S::kTok);
     const int64_t tiles = (int64_t)p.chan_tiles * p.tok_tiles;
     if (tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
     CUtensorMap mapW, mapA;
-    if (!code_map(&mapW, W, p.N, p.K, kChan) || !code_map(&mapA, A, p.T, p.K, S::kTokRows)) return cudaErrorInvalidValue;
+    if (!code_map(&mapW, W, p.N, p.K, kChan) || !code_map(&mapA, A, p.T, p.K, S::kTok)) return cudaErrorInvalidValue;
 
     const int sms = device_sm_count(), pairs = (p.K + 511) / 512;
-    int ranks = S::kPair ? 2 : 1;
+    int ranks = 1;
     if (S::kSplit)  // CTAs that share a tile: as many as still fit the GPU, and have work
         while (ranks < 8 && (ranks + 1) * tiles <= sms && ranks < pairs) ++ranks;
     cudaLaunchConfig_t cfg = {};
-    const int64_t clusters = S::kSplit || tiles < sms / ranks ? tiles : sms / ranks;
-    cfg.gridDim = dim3((unsigned)(clusters * ranks));
+    cfg.gridDim = dim3((unsigned)(S::kSplit ? tiles * ranks : tiles < sms ? tiles : sms));
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmemBytes;
     cfg.stream = s;
@@ -721,30 +685,29 @@ cudaError_t product(const uint8_t* A, const uint8_t* W, ProductArgs p, cudaStrea
     attr[1].val.clusterDim.x = (unsigned)ranks;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = S::kSplit ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, mapW, mapA, p);
 }
 
-using Split16 = ProductShape<16, 9, false>;
-using Split64 = ProductShape<64, 6, false>;
-// Four stages with the mix, whose loads of the streams need the L1 that a fifth
-// would take: 317 us against 345 at 16384 x 4096 x 8192.  Without it five are
-// a little faster: 110 against 113 at 8192 x 8192 x 4096.
-template <bool kMix>
-using Pair192 = ProductShape<192, kMix ? 4 : 5, true>;
+using Split16 = ProductShape<16, 9, true>;
+using Split64 = ProductShape<64, 6, true>;
+// Four stages of 40 KB; with three the products wait for their operands: 115 us
+// against 140 at 8192 x 8192 x 4096, with the mix 325 against 388 at 16384 x
+// 4096 x 8192, though its loads of the streams have the least L1 beside four.
+using Whole192 = ProductShape<192, 4, false>;
 
 // The form by size.  Split forms run one wave of clusters, so they are taken
 // while their tiles fit the GPU at once, and the narrowest that holds the
 // tokens: at N = 8192, K = 4096 one token takes 7.9 us in tiles of 16 and
 // 9.2 in tiles of 64; 200 tokens take 17.6 us in tiles of 64 (256 tiles, two
-// waves) and 13.4 in pairs.
+// waves) and 11.5 whole.
 template <bool kMix>
 cudaError_t product_by_size(const uint8_t* A, const uint8_t* W, const ProductArgs& p, cudaStream_t s)
 {
     const int64_t chan_tiles = (p.N + kChan - 1) / kChan, sms = device_sm_count();
     if (p.T <= 16 && chan_tiles <= sms) return product<Split16, kMix>(A, W, p, s);
     if (chan_tiles * ((p.T + 63) / 64) <= sms) return product<Split64, kMix>(A, W, p, s);
-    return product<Pair192<kMix>, kMix>(A, W, p, s);
+    return product<Whole192, kMix>(A, W, p, s);
 }
 
 }  // namespace

@@ -24,34 +24,19 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// At a barrier of another CTA of the cluster (an address of map_rank's).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// kCluster: also sees what other CTAs of the cluster did before they arrived.
-template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    if constexpr (kCluster)
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(ok)
-                     : "r"(bar), "r"(parity)
-                     : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(ok)
-                     : "r"(bar), "r"(parity)
-                     : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
     return ok != 0;
 }
 __device__ __forceinline__ uint64_t global_ns()
@@ -64,26 +49,24 @@ __device__ __forceinline__ uint64_t global_ns()
 // Waits until the barrier's phase of this parity is over, for at most `ns`
 // nanoseconds or until another role of the CTA has given up (abort not null and
 // *abort != 0).  false: it is not over.
-template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort,
                                           uint64_t ns = 2000000000ull)
 {
-    if (mbar_try<kCluster>(bar, parity)) return true;
+    if (mbar_try(bar, parity)) return true;
     const uint64_t t0 = global_ns();
-    while (!mbar_try<kCluster>(bar, parity))
+    while (!mbar_try(bar, parity))
         if ((abort != nullptr && *abort != 0) || global_ns() - t0 > ns)
-            return mbar_try<kCluster>(bar, parity);
+            return mbar_try(bar, parity);
     return true;
 }
 
 // The same for a whole warp; the answer is the warp's, and the compiler knows
 // it, so the operands of tensor instructions stay in uniform registers in the
 // code that follows.
-template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort)
 {
-    if (__all_sync(0xffffffffu, mbar_try<kCluster>(bar, parity))) return true;
-    return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, abort));
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
 // One lane of a whole warp.  Written as a predicate around single
@@ -120,28 +103,17 @@ __device__ __forceinline__ void prefetch_map(const void* map)
 
 // -------------------------------------------------------------- tensor memory
 
-// kPair throughout: the forms for two CTAs that work on one tile, where the CTA
-// of rank 0 issues for both.  A kernel uses one form only.
-template <int kColumns, bool kPair>
-__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem)  // one whole warp (of each CTA)
+template <int kColumns>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem)  // one whole warp
 {
-    if constexpr (kPair) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "n"(kColumns)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-    } else {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "n"(kColumns)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "n"(kColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
 }
-template <int kColumns, bool kPair>
+template <int kColumns>
 __device__ __forceinline__ void tmem_free(uint32_t base)  // the same warp
 {
-    if constexpr (kPair)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(kColumns));
-    else
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(kColumns));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(kColumns));
 }
 __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before_sync()
@@ -180,15 +152,10 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr)
 }
 
 // 512 bytes of scales into four columns: row r of 32 in lane r, the same in
-// each of the four groups of 32 lanes.  A pair: in both CTAs, each from its own
-// shared memory.
-template <bool kPair>
+// each of the four groups of 32 lanes.
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc)
 {
-    if constexpr (kPair)
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-    else
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
 // Instruction descriptor of a product of e2m1 operands (both K-major, fp32
@@ -200,48 +167,22 @@ __host__ __device__ constexpr uint32_t mx4_instruction(int M, int N)
 }
 __host__ __device__ constexpr uint32_t scale_select(int sf) { return (uint32_t)sf << 4 | (uint32_t)sf << 29; }
 
-// One step of 64 along K.  A pair: the CTAs' row tiles side by side as 2 M
-// rows, each CTA holding half of the columns' operand and the sums of its rows.
-template <bool kPair>
+// One step of 64 along K.
 __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t inst, uint32_t sa, uint32_t sb,
                                         bool accumulate)
 {
-    if constexpr (kPair)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                         "r"(d),
-                     "l"(a), "l"(b), "r"(inst), "r"(sa), "r"(sb), "r"((uint32_t)accumulate)
-                     : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                         "r"(d),
-                     "l"(a), "l"(b), "r"(inst), "r"(sa), "r"(sb), "r"((uint32_t)accumulate)
-                     : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                     "r"(d),
+                 "l"(a), "l"(b), "r"(inst), "r"(sa), "r"(sb), "r"((uint32_t)accumulate)
+                 : "memory");
 }
-// Arrives at the barrier once all tcgen05 work of this thread so far is done (at
-// once where there is none); commit_both at the barriers of that offset in both
-// CTAs of a pair.
-template <bool kPair>
+// Arrives at the barrier once all tcgen05 work of this thread so far is done.  It
+// orders that work only: what a thread knows of other writes it passes on by
+// mbar_arrive.
 __device__ __forceinline__ void commit(uint32_t bar)
 {
-    if constexpr (kPair)
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                     : "memory");
-    else
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                     : "memory");
-}
-template <bool kPair>
-__device__ __forceinline__ void commit_both(uint32_t bar)
-{
-    if constexpr (kPair)
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::
-                         "r"(bar),
-                     "h"((uint16_t)3)
-                     : "memory");
-    else
-        commit<false>(bar);
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // -------------------------------------------------------------------- cluster
