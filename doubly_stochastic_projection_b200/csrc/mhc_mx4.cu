@@ -117,7 +117,7 @@ constexpr int kRowBytes = 128;  // of K of a tile: 256 elements
 constexpr int kEpiWarps = 8;
 constexpr int kEpiThreads = 32 * kEpiWarps;
 
-constexpr uint64_t kDrainNs = 100000000;  // for what is in flight, once a wait has run out
+constexpr uint64_t kDrainNs = 100000000;  // for all that is in flight, once a wait has run out
 
 __device__ int mx4_wait_expired;
 
@@ -340,10 +340,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
     bool ok = true;
 
     const int mine = first < tiles ? (tiles - 1 - first) / stride + 1 : 0, steps = k1 - k0;  // output tiles, K tiles
+    int64_t loads = 0;  // warp 0's, so far
     if (warp == 0) {
         int s = 0, t = first;
         uint32_t phase = 0;
-        int64_t loads = 0;
         for (int n = 0; n < mine && ok; ++n, t += stride) {
             const int n0 = t % p.chan_tiles * kChan, t0 = t / p.chan_tiles * kTok;
             for (int k = k0; k < k1; ++k, ++loads) {
@@ -358,11 +358,6 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 s = s + 1 == kStages ? 0 : s + 1;
                 phase ^= s == 0;
             }
-        }
-        if (!ok) {
-            *abort = 1;  // the copies in flight: the last kStages at most
-            for (int64_t j = loads > kStages ? loads - kStages : 0; j < loads; ++j)
-                tc5::mbar_wait(full((int)(j % kStages)), (uint32_t)(j / kStages) & 1, nullptr, kDrainNs);
         }
     } else if (warp == 2) {
         // each K tile's scales from shared into tensor memory, ahead of the products
@@ -390,12 +385,6 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 buf ^= last;
                 par ^= last && buf == 0;
             }
-        }
-        if (!ok) {
-            *abort = 1;
-            if (tc5::elect_one()) tc5::commit(drained);
-            __syncwarp();
-            tc5::mbar_wait(drained, 0, nullptr, kDrainNs);
         }
     } else if (warp == 1) {
         // The whole warp waits, one lane issues.  The queue behind it is short
@@ -439,12 +428,6 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 __syncwarp();
                 if (!ok) break;
             }
-        }
-        if (!ok) {
-            *abort = 1;  // the tensor work in flight, before its memory is freed
-            if (tc5::elect_one()) tc5::commit(drained);
-            __syncwarp();
-            tc5::mbar_wait(drained, 0, nullptr, kDrainNs);
         }
     } else if (warp == 3 || warp >= 12) {
         // warp 3: W's rows, the others: 128 of A's each; lane l holds rows l, l + 32,
@@ -507,11 +490,19 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 par ^= buf == 0;
             }
         }
-        if (!ok) *abort = 1;
     } else {
         const int e = threadIdx.x - 128;  // 0..255
         const int quarter = warp & 3, half = (warp - 4) >> 2;  // lanes of tensor memory that a warp may read
         const uint32_t row = (uint32_t)(32 * quarter) << 16;
+        // sums that may still be in work, as a wait has run out, are not read
+        const auto load_sums = [&](int a, int g, float(&v)[16]) {
+            if (ok) {
+                tc5::tmem_load(tmem + row + a * kTok + g, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = __int_as_float(0x7fffffff);
+            }
+        };
         int n = 0;
         for (int tile = first; tile < tiles; tile += stride, ++n) {
             const int a = n % S::kSums;
@@ -524,10 +515,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
 #pragma unroll 1
                 for (int g = 16 * half; g < kTok; g += 32) {
                     float v[16];
-                    tc5::tmem_load(tmem + row + a * kTok + g, v);
+                    load_sums(a, g, v);
                     float* to = epi + g * kChan + 32 * quarter + lane;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) to[i * kChan] = ok ? v[i] : __int_as_float(0x7fffffff);
+                    for (int i = 0; i < 16; ++i) to[i * kChan] = v[i];
                 }
             } else {
 #pragma unroll 1
@@ -543,7 +534,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                         if (in[i]) x[i].load(p, t, vec);
                     }
                     float v[16];
-                    tc5::tmem_load(tmem + row + a * kTok + g + 16 * half, v);
+                    load_sums(a, g + 16 * half, v);
                     if (g + S::kGroup >= kTok) {  // the last read of this tile's sums
                         tc5::fence_before_sync();
                         __syncwarp();
@@ -553,7 +544,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                     float* buf = epi + (g & S::kGroup) * kChan;
                     float* to = buf + 16 * half * kChan + 32 * quarter + lane;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) to[i * kChan] = ok ? v[i] : __int_as_float(0x7fffffff);
+                    for (int i = 0; i < 16; ++i) to[i * kChan] = v[i];
                     asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -566,9 +557,11 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 }
             }
         }
-        if (!ok) *abort = 1;
     }
-    if (!ok) mx4_wait_expired = 1;
+    if (!ok) {
+        *abort = 1;
+        mx4_wait_expired = 1;
+    }
     __syncwarp();
 
     if (S::kSplit) {
@@ -597,6 +590,23 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
     }
     tc5::fence_before_sync();
     __syncthreads();
+    if (*abort != 0) {
+        // A wait of some role has run out, so nothing says that the others' work is
+        // done, not even where they had no wait left: before its shared and tensor
+        // memory go, the copies in flight (the last kStages at most) and the tensor
+        // work are waited for
+        const uint64_t t0 = tc5::global_ns();
+        const auto left = [&] { return kDrainNs - min(kDrainNs, tc5::global_ns() - t0); };
+        if (warp == 0) {
+            for (int64_t j = loads > kStages ? loads - kStages : 0; j < loads; ++j)
+                tc5::mbar_wait(full((int)(j % kStages)), (uint32_t)(j / kStages) & 1, nullptr, left());
+        } else if (warp <= 2) {
+            if (tc5::elect_one()) tc5::commit(drained);
+            __syncwarp();
+            tc5::mbar_wait(drained, 0, nullptr, left());
+        }
+        __syncthreads();
+    }
     if (warp == 1) {
         tc5::fence_after_sync();
         tc5::tmem_free<S::kColumns>(tmem);

@@ -21,3 +21,20 @@ def test_no_operand_waits_for_word_of_another_cta():
     assert all(m.startswith("map_rank(tc5::smem_addr(epi") for m in re.findall(r"map_rank\([^)]*\)?", product))
     for bar in re.findall(r"(?:commit|mbar_arrive|mbar_expect_tx)\w*(?:<\w+>)?\(([^;]*);", product):
         assert "map_rank" not in bar, bar
+
+
+def test_a_wait_that_ran_out_leaves_nothing_in_flight():
+    # a role that has no wait left does not learn in its own code that another
+    # gave up: what is in flight is waited for behind a barrier of the CTA, by the
+    # roles that issue it, whether their own waits ran out or not
+    product = _read("mhc_mx4.cu")
+    kernel = product[product.index("mx4_product_kernel(const __grid_constant__"):product.index("tmem_free")]
+    assert kernel.count("commit(drained)") == 1
+    way_out = kernel[kernel.rindex("tc5::fence_before_sync();"):]
+    barrier, check, again = (way_out.index(x) for x in ("__syncthreads();", "if (*abort != 0)", "__syncthreads();\n    }"))
+    assert barrier < check < again
+    drain = way_out[check:again]
+    assert "if (!ok)" not in drain and "if (ok)" not in drain
+    assert "warp == 0" in drain and "mbar_wait(full(" in drain and "commit(drained)" in drain
+    # nor are sums read that may still be in work
+    assert re.search(r"if \(ok\) \{\s*tc5::tmem_load", kernel) and kernel.count("tmem_load(") == 1
