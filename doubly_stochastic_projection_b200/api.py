@@ -81,6 +81,7 @@ def lib() -> ctypes.CDLL:
                 "mhc_premap_fwd_mx4": [p, p, p, p, i64, i64, p],
                 "mhc_wait_status": [],
                 "mhc_mx4_linear": [p, p, p, p, p, i64, i64, i64, p],
+                "mhc_mx4_linear_diag": [p, p, p, p, p, i64, i64, i64, i64, i32, p],
                 "mhc_mx4_linear_mix": [p, p, p, p, p, p, p, p, i64, i64, i64, p],
                 "mhc_residual_mix_fwd": [p, p, p, p, p, i64, i64, p],
                 "mhc_residual_mix_bwd": [p, p, p, p, p, p, p, p, p, p, i64, i64, p],
@@ -734,9 +735,27 @@ def mx4_linear_mix(a: MxTensor, w: MxTensor, X, H_res, h_post, out=None):
     return out
 
 
+MX4_ROLES = {"loads": 1, "products": 2, "copies": 4, "scales": 8}
+
+
+def mx4_linear_diag(a: MxTensor, w: MxTensor, wait_ns: int = 2_000_000_000, idle=(), out=None):
+    """mx4_linear whose waits end after wait_ns nanoseconds, and with roles of its
+    kernel (names of MX4_ROLES) left out, for which the others wait in vain: for
+    tests of what becomes of a wait that runs out (wait_status)."""
+    T, N, K = _product_shapes(a, w)
+    if out is None:
+        out = a.codes.new_empty((T, N), dtype=torch.bfloat16)
+    else:
+        _need(out, "out", torch.bfloat16, (T, N))
+    mask = sum({MX4_ROLES[r] for r in idle})
+    _launch(lib().mhc_mx4_linear_diag, (a[0], a[1], w[0], w[1], out), T, N, K, int(wait_ns), mask)
+    return out
+
+
 def wait_status() -> None:
-    """Raises MhcError if a bounded wait of the 4-bit products has run out on the
-    current device since the last call (mhc_wait_status); synchronises the device."""
+    """Raises MhcError (status 6) if a bounded wait of the 4-bit products has run
+    out on the current device since the last call (mhc_wait_status); synchronises
+    the device."""
     _check(lib().mhc_wait_status())
 
 

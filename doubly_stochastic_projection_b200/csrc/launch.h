@@ -87,6 +87,11 @@ cudaError_t launch_mx4_linear(const uint8_t* A, const uint8_t* As, const uint8_t
 cudaError_t launch_mx4_linear_mix(const uint8_t* A, const uint8_t* As, const uint8_t* W, const uint8_t* Ws,
                                   const uint16_t* X, const float* H, const float* hpost, uint16_t* Y, int64_t T,
                                   int64_t C, int64_t K, cudaStream_t s);
+constexpr int64_t kProductWaitNs = 2000000000;  // limit of a wait in the products
+// With another limit, and roles (`idle`: enum mhc_mx4_role) that do nothing.
+cudaError_t launch_mx4_linear_diag(const uint8_t* A, const uint8_t* As, const uint8_t* W, const uint8_t* Ws,
+                                   uint16_t* out, int64_t T, int64_t N, int64_t K, int64_t wait_ns, int idle,
+                                   cudaStream_t s);
 
 // Whether a bounded wait of the 4-bit products has run out since the last
 // call; synchronises the device.

@@ -73,6 +73,7 @@ const char* mhc_status_string(int status)
     case MHC_ERR_SIZE: return "MHC_ERR_SIZE: negative or unsupported size (C must be a positive multiple of 8)";
     case MHC_ERR_ARG: return "MHC_ERR_ARG: unknown method or iteration count out of range";
     case MHC_ERR_CUDA: return "MHC_ERR_CUDA: the CUDA runtime reported a launch error";
+    case MHC_ERR_WAIT: return "MHC_ERR_WAIT: a bounded wait on the device ran out";
     default: return "unknown mhc status";
     }
 }
@@ -429,6 +430,23 @@ int mhc_mx4_linear(const uint8_t* A_codes, const uint8_t* A_scales, const uint8_
                                               static_cast<cudaStream_t>(stream)));
 }
 
+int mhc_mx4_linear_diag(const uint8_t* A_codes, const uint8_t* A_scales, const uint8_t* W_codes,
+                        const uint8_t* W_scales, uint16_t* out, int64_t T, int64_t N, int64_t K, int64_t wait_ns,
+                        int idle, void* stream)
+{
+    int rc = check_product_sizes(T, N, K);
+    if (rc != MHC_OK) return rc;
+    if (wait_ns < 1 || wait_ns > mhc::kProductWaitNs || idle < 0 ||
+        idle > (MHC_MX4_LOADS | MHC_MX4_PRODUCTS | MHC_MX4_COPIES | MHC_MX4_SCALES))
+        return MHC_ERR_ARG;
+    if (T == 0) return MHC_OK;
+    if (!A_codes || !A_scales || !W_codes || !W_scales || !out) return MHC_ERR_NULL;
+    if (misaligned(A_codes) || misaligned(A_scales) || misaligned(W_codes) || misaligned(W_scales) || misaligned(out))
+        return MHC_ERR_ALIGN;
+    return cuda_status(mhc::launch_mx4_linear_diag(A_codes, A_scales, W_codes, W_scales, out, T, N, K, wait_ns, idle,
+                                                   static_cast<cudaStream_t>(stream)));
+}
+
 int mhc_mx4_linear_mix(const uint8_t* A_codes, const uint8_t* A_scales, const uint8_t* W_codes,
                        const uint8_t* W_scales, const uint16_t* X, const float* H_res, const float* h_post,
                        uint16_t* Y, int64_t T, int64_t C, int64_t K, void* stream)
@@ -449,7 +467,7 @@ int mhc_wait_status(void)
 {
     bool expired = false;
     const cudaError_t e = mhc::read_wait_status(&expired);
-    return e != cudaSuccess || expired ? MHC_ERR_CUDA : MHC_OK;
+    return e != cudaSuccess ? cuda_status(e) : expired ? MHC_ERR_WAIT : MHC_OK;
 }
 
 int mhc_composite_gain(const float* P_layers, float* M, float* gain_rows, float* gain_cols, int64_t L, int64_t T,

@@ -129,6 +129,8 @@ struct ProductArgs {
     int64_t T;
     int N, K;
     int chan_tiles, tok_tiles;
+    uint64_t wait_ns;  // kDiag: limit of a wait
+    int idle;          // kDiag: enum mhc_mx4_role
 };
 
 template <int kTok_, int kStages_, bool kSplit_>
@@ -276,7 +278,9 @@ struct StreamVec<true> {
     }
 };
 
-template <class S, bool kMix>
+// kDiag (a kernel of its own, as the mask costs each product 0.2 to 0.4 us): with a
+// limit of the caller's for the waits, and roles that do nothing.
+template <class S, bool kMix, bool kDiag>
 __global__ void __launch_bounds__(S::kThreads, 1)
 mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapA,
                    const ProductArgs p)
@@ -335,8 +339,15 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
     const int pairs = (p.K + 511) / 512;  // 16 bytes of scales
     const int pair0 = pairs * rank / ranks, pair1 = pairs * (rank + 1) / ranks;
     const int k0 = 2 * pair0, k1 = min(2 * pair1, (p.K + 255) / 256);
-    const int tiles = p.chan_tiles * p.tok_tiles;
     const int first = blockIdx.x / ranks, stride = gridDim.x / ranks;
+    const uint64_t wait_ns = kDiag ? p.wait_ns : (uint64_t)kProductWaitNs;
+    int tiles = p.chan_tiles * p.tok_tiles;
+    if (kDiag) {
+        const int role = warp == 0 ? MHC_MX4_LOADS : warp == 1 ? MHC_MX4_PRODUCTS : warp == 2 ? MHC_MX4_COPIES
+                         : warp == 3 || warp >= 12                                            ? MHC_MX4_SCALES
+                                                                                              : 0;
+        if ((p.idle & role) != 0) tiles = 0;
+    }
     bool ok = true;
 
     const int mine = first < tiles ? (tiles - 1 - first) / stride + 1 : 0, steps = k1 - k0;  // output tiles, K tiles
@@ -347,7 +358,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         for (int n = 0; n < mine && ok; ++n, t += stride) {
             const int n0 = t % p.chan_tiles * kChan, t0 = t / p.chan_tiles * kTok;
             for (int k = k0; k < k1; ++k, ++loads) {
-                if (!(ok = tc5::mbar_wait_warp(empty(s), phase ^ 1, abort))) break;
+                if (!(ok = tc5::mbar_wait_warp(empty(s), phase ^ 1, abort, wait_ns))) break;
                 const uint32_t at = base + s * S::kStageBytes;
                 if (tc5::elect_one()) {
                     tc5::mbar_expect_tx(full(s), S::kWBytes + S::kABytes);
@@ -366,8 +377,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         for (int n = 0; n < mine && ok; ++n) {
             for (int k = 0; k < steps; ++k) {
                 const int j = k & (S::kBufTiles - 1);  // in this buffer
-                if (j == 0 && !(ok = tc5::mbar_wait_warp(scales_full(buf), par, abort))) break;
-                if (!(ok = tc5::mbar_wait_warp(empty(s), phase ^ 1, abort))) break;
+                if (j == 0 && !(ok = tc5::mbar_wait_warp(scales_full(buf), par, abort, wait_ns))) break;
+                if (!(ok = tc5::mbar_wait_warp(empty(s), phase ^ 1, abort, wait_ns))) break;
                 tc5::fence_after_sync();
                 const uint32_t at = base + kOffScales + (buf * S::kBufSteps + 2 * j) * S::kScaleStep;
                 const uint32_t sw = tmem + S::kSumCols + s * S::kScaleCols;
@@ -393,10 +404,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
         constexpr uint32_t inst = tc5::mx4_instruction(kChan, kTok);
         int s = 0;
         uint32_t phase = 0;
-        if (mine > 0) ok = tc5::mbar_wait_warp(full(0), 0, abort);
+        if (mine > 0) ok = tc5::mbar_wait_warp(full(0), 0, abort, wait_ns);
         for (int n = 0; n < mine && ok; ++n) {
             const int a = n % S::kSums;
-            if (!(ok = tc5::mbar_wait_warp(sum_empty(a), (n / S::kSums & 1) ^ 1, abort))) break;
+            if (!(ok = tc5::mbar_wait_warp(sum_empty(a), (n / S::kSums & 1) ^ 1, abort, wait_ns))) break;
             const uint32_t d = tmem + a * kTok;
             for (int k = 0; k < steps; ++k) {
                 tc5::fence_after_sync();
@@ -419,7 +430,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                 }
                 __syncwarp();
                 // the next K tile's wait, while the queue holds steps of this one
-                if (k + 1 < steps || n + 1 < mine) ok = tc5::mbar_wait_warp(full(s), phase, abort);
+                if (k + 1 < steps || n + 1 < mine) ok = tc5::mbar_wait_warp(full(s), phase, abort, wait_ns);
                 if (tc5::elect_one()) {
                     step(3);
                     tc5::commit(empty(here));
@@ -468,7 +479,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
                     fetch(tile, pair + 2);
                 else
                     fetch(tile + stride, pair0);
-                if (!(ok = tc5::mbar_wait_warp(scales_empty(buf), par ^ 1, abort))) break;
+                if (!(ok = tc5::mbar_wait_warp(scales_empty(buf), par ^ 1, abort, wait_ns))) break;
 #pragma unroll
                 for (int j = 0; j < S::kBufSteps; ++j) {  // steps of 128 elements, one word of scales a row
                     const int w0 = 4 * pair + j;
@@ -508,7 +519,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_consta
             const int a = n % S::kSums;
             const int v0 = tile % p.chan_tiles * (kChan / 8);
             const int64_t t0 = (int64_t)(tile / p.chan_tiles) * kTok;
-            if (ok) ok = tc5::mbar_wait_warp(sum_full(a), n / S::kSums & 1, abort);
+            if (ok) ok = tc5::mbar_wait_warp(sum_full(a), n / S::kSums & 1, abort, wait_ns);
             tc5::fence_after_sync();
             if (S::kSplit) {
                 // each token in its place, for the cluster to add up
@@ -659,10 +670,10 @@ bool code_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, i
                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class S, bool kMix>
+template <class S, bool kMix, bool kDiag>
 cudaError_t product(const uint8_t* A, const uint8_t* W, ProductArgs p, cudaStream_t s)
 {
-    const auto kernel = mx4_product_kernel<S, kMix>;
+    const auto kernel = mx4_product_kernel<S, kMix, kDiag>;
     static std::atomic<uint64_t> allowed{0};  // devices whose shared-memory limit is set for this kernel
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -711,13 +722,13 @@ using Whole192 = ProductShape<192, 4, false>;
 // tokens: at N = 8192, K = 4096 one token takes 7.9 us in tiles of 16 and
 // 9.2 in tiles of 64; 200 tokens take 17.6 us in tiles of 64 (256 tiles, two
 // waves) and 11.5 whole.
-template <bool kMix>
+template <bool kMix, bool kDiag = false>
 cudaError_t product_by_size(const uint8_t* A, const uint8_t* W, const ProductArgs& p, cudaStream_t s)
 {
     const int64_t chan_tiles = (p.N + kChan - 1) / kChan, sms = device_sm_count();
-    if (p.T <= 16 && chan_tiles <= sms) return product<Split16, kMix>(A, W, p, s);
-    if (chan_tiles * ((p.T + 63) / 64) <= sms) return product<Split64, kMix>(A, W, p, s);
-    return product<Whole192, kMix>(A, W, p, s);
+    if (p.T <= 16 && chan_tiles <= sms) return product<Split16, kMix, kDiag>(A, W, p, s);
+    if (chan_tiles * ((p.T + 63) / 64) <= sms) return product<Split64, kMix, kDiag>(A, W, p, s);
+    return product<Whole192, kMix, kDiag>(A, W, p, s);
 }
 
 }  // namespace
@@ -726,7 +737,17 @@ cudaError_t launch_mx4_linear(const uint8_t* A, const uint8_t* As, const uint8_t
                               int64_t T, int64_t N, int64_t K, cudaStream_t s)
 {
     return product_by_size<false>(
-        A, W, ProductArgs{As, Ws, (uint4*)out, nullptr, nullptr, nullptr, T, (int)N, (int)K, 0, 0}, s);
+        A, W, ProductArgs{As, Ws, (uint4*)out, nullptr, nullptr, nullptr, T, (int)N, (int)K, 0, 0, 0, 0}, s);
+}
+
+cudaError_t launch_mx4_linear_diag(const uint8_t* A, const uint8_t* As, const uint8_t* W, const uint8_t* Ws,
+                                   uint16_t* out, int64_t T, int64_t N, int64_t K, int64_t wait_ns, int idle,
+                                   cudaStream_t s)
+{
+    return product_by_size<false, true>(A, W,
+                                        ProductArgs{As, Ws, (uint4*)out, nullptr, nullptr, nullptr, T, (int)N, (int)K,
+                                                    0, 0, (uint64_t)wait_ns, idle},
+                                        s);
 }
 
 cudaError_t launch_mx4_linear_mix(const uint8_t* A, const uint8_t* As, const uint8_t* W, const uint8_t* Ws,
@@ -734,7 +755,7 @@ cudaError_t launch_mx4_linear_mix(const uint8_t* A, const uint8_t* As, const uin
                                   int64_t C, int64_t K, cudaStream_t s)
 {
     return product_by_size<true>(
-        A, W, ProductArgs{As, Ws, (uint4*)Y, (const uint4*)X, H, hpost, T, (int)C, (int)K, 0, 0}, s);
+        A, W, ProductArgs{As, Ws, (uint4*)Y, (const uint4*)X, H, hpost, T, (int)C, (int)K, 0, 0, 0, 0}, s);
 }
 
 // The status of the bounded waits since the last call (synchronises the device).

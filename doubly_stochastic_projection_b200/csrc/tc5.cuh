@@ -49,8 +49,7 @@ __device__ __forceinline__ uint64_t global_ns()
 // Waits until the barrier's phase of this parity is over, for at most `ns`
 // nanoseconds or until another role of the CTA has given up (abort not null and
 // *abort != 0).  false: it is not over.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort,
-                                          uint64_t ns = 2000000000ull)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t ns)
 {
     if (mbar_try(bar, parity)) return true;
     const uint64_t t0 = global_ns();
@@ -63,10 +62,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // The same for a whole warp; the answer is the warp's, and the compiler knows
 // it, so the operands of tensor instructions stay in uniform registers in the
 // code that follows.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort)
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t ns)
 {
     if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, ns));
 }
 
 // One lane of a whole warp.  Written as a predicate around single

@@ -72,7 +72,8 @@ enum mhc_status {
     MHC_ERR_ALIGN = 2, /* a pointer is not 16-byte aligned                   */
     MHC_ERR_SIZE = 3,  /* negative size, C <= 0 or C % 8 != 0, or too large  */
     MHC_ERR_ARG = 4,   /* unknown method or iteration count out of range     */
-    MHC_ERR_CUDA = 5   /* the CUDA runtime reported an error at launch       */
+    MHC_ERR_CUDA = 5,  /* the CUDA runtime reported an error at launch       */
+    MHC_ERR_WAIT = 6   /* a bounded wait on the device ran out (mhc_wait_status) */
 };
 
 /* Forward solvers. */
@@ -477,11 +478,30 @@ MHC_API int mhc_mx4_linear_mix(const uint8_t *A_codes, const uint8_t *A_scales, 
  * mhc_wait_status -- diagnostic of the products: their kernels hand tiles from
  * one warp to another through waits that end after two seconds at most.  A
  * wait that runs out means a fault of the device or a defect, not a bad
- * argument; the outputs that were not done are NaN.  Returns MHC_ERR_CUDA if
- * that happened on the current device since the last call, MHC_OK otherwise.
- * Synchronises the device: not for use during stream capture.
+ * argument; the outputs that were not done are NaN.  Returns MHC_ERR_WAIT if
+ * that happened on the current device since the last call, MHC_ERR_CUDA if the
+ * device cannot be asked, MHC_OK otherwise.  Synchronises the device: not for
+ * use during stream capture.
  */
 MHC_API int mhc_wait_status(void);
+
+/*
+ * mhc_mx4_linear_diag -- mhc_mx4_linear with a limit of one's own for its waits,
+ * and with roles of its kernel left out, for whose work the others then wait in
+ * vain: what a test needs to see a wait run out.
+ *
+ *   wait_ns  limit of each wait, 1 .. 2000000000 (MHC_ERR_ARG otherwise).
+ *   idle     sum of enum mhc_mx4_role; 0 for none (MHC_ERR_ARG past their sum).
+ */
+enum mhc_mx4_role {
+    MHC_MX4_LOADS = 1,    /* the codes' copies into shared memory          */
+    MHC_MX4_PRODUCTS = 2, /* the products                                  */
+    MHC_MX4_COPIES = 4,   /* the scales' copies into tensor memory         */
+    MHC_MX4_SCALES = 8    /* the scales' loads                             */
+};
+MHC_API int mhc_mx4_linear_diag(const uint8_t *A_codes, const uint8_t *A_scales, const uint8_t *W_codes,
+                                const uint8_t *W_scales, uint16_t *out, int64_t T, int64_t N, int64_t K,
+                                int64_t wait_ns, int idle, void *stream);
 
 /*
  * mhc_composite_gain -- diagnostic of the composite mixing map across depth:

@@ -85,3 +85,18 @@ def test_scale_pitch_is_the_header_s():
     text = open(build.INCLUDE + "/mhc_birkhoff.h").read()
     assert re.search(r"#define MHC_MX_SCALE_PITCH\(C\) \(4 \* \(\(\(int64_t\)\(C\) \+ 127\) / 128\)\)", text)
     assert [api.mx_scale_pitch(C) for C in (8, 32, 128, 136, 4096)] == [4, 4, 4, 8, 128]
+
+
+def test_waits_that_run_out_have_a_status_of_their_own(L):
+    L.mhc_status_string.restype = ctypes.c_char_p
+    L.mhc_status_string.argtypes = [ctypes.c_int]
+    assert b"MHC_ERR_WAIT" in L.mhc_status_string(6)
+    f = entry(L, "mhc_mx4_linear_diag", 5, [I64, I64, I64, I64, I32])
+    a = [FAKE] * 5
+    assert f(*a, 4, 12, 64, 1000, 0, None) == SIZE
+    for wait_ns, idle in [(0, 0), (-1, 0), (2_000_000_001, 0), (1000, -1), (1000, 16)]:
+        assert f(*a, 4, 64, 64, wait_ns, idle, None) == ARG, (wait_ns, idle)
+    assert f(*[None] * 5, 0, 64, 64, 1000, 1, None) == OK
+    for k in range(5):
+        assert f(*[None if i == k else FAKE for i in range(5)], 4, 64, 64, 1000, 1, None) == NULL
+        assert f(*[FAKE + 2 if i == k else FAKE for i in range(5)], 4, 64, 64, 1000, 1, None) == ALIGN

@@ -438,6 +438,28 @@ def test_serving_layer_runs_together():
         assert (np.abs(to_np64(Y) - ref) <= tol).all()
 
 
+@pytest.mark.parametrize("role", sorted(api.MX4_ROLES))
+@pytest.mark.parametrize("T,N,K", [(3, 264, 2080), (3, 264, 32768), (60, 264, 32768), (1500, 2056, 4128)])
+def test_a_wait_that_runs_out(T, N, K, role):
+    # a role that does nothing: the others wait for it in vain, each for a
+    # millisecond, and return.  In all three forms, with K tiles for each stage and
+    # more, and (the first) with so few that some role has no wait left
+    a, w = _operands(T, N, K, 81)
+    ref = api.mx4_linear(a, w)
+    api.wait_status()
+    out = torch.full((T + 1, N), 7.0, dtype=torch.bfloat16, device=dev())
+    api.mx4_linear_diag(a, w, wait_ns=1_000_000, idle=(role,), out=out[:T])
+    with pytest.raises(api.MhcError) as e:
+        api.wait_status()
+    assert e.value.status == 6
+    api.wait_status()  # said once
+    assert torch.isnan(out[:T]).all() and (out[T:] == 7).all()
+    # the next product has its shared and tensor memory whole, on every SM
+    assert torch.equal(api.mx4_linear(a, w), ref)
+    assert torch.equal(api.mx4_linear_diag(a, w), ref)
+    api.wait_status()
+
+
 # ---------------------------------------------------- streams, graphs, refusals
 
 def test_side_streams_and_graph_replay():
