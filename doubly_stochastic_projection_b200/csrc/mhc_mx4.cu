@@ -167,21 +167,22 @@ struct ProductShape {
 // since every lane reads another row and each load costs a pass over 32 cache
 // lines (which the 32-byte form, done with its sector, does not keep).  Words past
 // the row read as zero.  Volatile, so that the loads stay where they are issued, a
-// round ahead of their use.
+// round ahead of their use.  Not the non-coherent form, here and for the mix's
+// maps: this kernel may start while the one that writes them still runs.
 __device__ __forceinline__ void fetch_scales(const uint8_t* row, int pair, bool two, int pitch, int align, uint4& q0,
                                              uint4& q1)
 {
     const uint8_t* at = row + 16 * pair;
     if (align == 32 && two) {
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(q0.x), "=r"(q0.y), "=r"(q0.z), "=r"(q0.w), "=r"(q1.x), "=r"(q1.y), "=r"(q1.z), "=r"(q1.w)
                      : "l"(at));
     } else if (align >= 16) {
-        asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(q0.x), "=r"(q0.y), "=r"(q0.z), "=r"(q0.w)
                      : "l"(at));
         if (two)
-            asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+            asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(q1.x), "=r"(q1.y), "=r"(q1.z), "=r"(q1.w)
                          : "l"(at + 16));
     } else {
@@ -190,7 +191,7 @@ __device__ __forceinline__ void fetch_scales(const uint8_t* row, int pair, bool 
         for (int j = 0; j < 8; ++j) {
             w[j] = 0u;
             if (16 * pair + 4 * j < pitch && (j < 4 || two))
-                asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(w[j]) : "l"(at + 4 * j));
+                asm volatile("ld.global.b32 %0, [%1];" : "=r"(w[j]) : "l"(at + 4 * j));
         }
         q0 = make_uint4(w[0], w[1], w[2], w[3]);
         q1 = make_uint4(w[4], w[5], w[6], w[7]);
@@ -247,7 +248,18 @@ struct StreamVec<true> {
         const int NV = p.N >> 3;
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = __ldcs(p.X + (t * 4 + j) * NV + v);
-        load_maps(p.H, p.hpost, t, h, hp);
+        const float4* H = reinterpret_cast<const float4*>(p.H) + 4 * t;
+        float4 q[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) q[i] = i < 4 ? H[i] : reinterpret_cast<const float4*>(p.hpost)[t];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            float* to = i < 4 ? h + 4 * i : hp;
+            to[0] = q[i].x;
+            to[1] = q[i].y;
+            to[2] = q[i].z;
+            to[3] = q[i].w;
+        }
     }
     __device__ __forceinline__ void emit(const ProductArgs& p, const float (&f)[8], int64_t t, int v) const
     {

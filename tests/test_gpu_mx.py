@@ -546,6 +546,43 @@ def test_product_follows_its_operands(T):
     del graph
 
 
+@pytest.mark.parametrize("K", (544, 1536, 2048))  # scale rows of 20, 48 and 64 bytes: loads of 4, 16 and 32
+@pytest.mark.parametrize("T,N", [(1, 1024), (40, 1024), (700, 2048)])
+def test_product_follows_its_scales_and_maps(T, N, K):
+    # as above, at every width of the scales' loads, and with maps and weights that
+    # the kernels just before it wrote
+    xs = [streams((T, K), 90 + i, outliers=False) for i in range(3)]
+    ws = [streams((N, K), 93 + i, outliers=False) for i in range(3)]
+    rng = np.random.default_rng(96)
+    lg = [to_gpu(rng.standard_normal((T, 4, 4)).astype(np.float32)) for _ in xs]
+    h = to_gpu(rng.uniform(0, 2, (T, 4)).astype(np.float32))
+    X = streams((T, 4, N), 97)
+    a, w, H = api.mx_pack(xs[0], "e2m1"), api.mx_pack(ws[0], "e2m1"), api.birkhoff_fwd(lg[0])
+
+    def chain(wait):
+        got = []
+        for x, wt, l in zip(xs, ws, lg):
+            steps = (lambda: api.mx_pack(wt, "e2m1", out=w), lambda: api.mx_pack(x, "e2m1", out=a),
+                     lambda: got.append(api.mx4_linear(a, w)), lambda: api.mx_pack(x, "e2m1", out=a),
+                     lambda: api.birkhoff_fwd(l, out=H), lambda: got.append(api.mx4_linear_mix(a, w, X, H, h)))
+            for f in steps:
+                f()
+                wait()
+        return got
+
+    ref = chain(torch.cuda.synchronize)
+    for _ in range(10):
+        assert all(torch.equal(g, r) for g, r in zip(chain(lambda: None), ref))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain(lambda: None)
+    for _ in range(10):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, r) for g, r in zip(out, ref))
+    del graph
+
+
 def test_empty_batches():
     d = dev()
     for fmt in FORMATS:

@@ -38,3 +38,12 @@ def test_a_wait_that_ran_out_leaves_nothing_in_flight():
     assert "warp == 0" in drain and "mbar_wait(full(" in drain and "commit(drained)" in drain
     # nor are sums read that may still be in work
     assert re.search(r"if \(ok\) \{\s*tc5::tmem_load", kernel) and kernel.count("tmem_load(") == 1
+
+
+def test_product_reads_through_the_coherent_path():
+    # the product may start while its producer still runs, so nothing that it reads
+    # is constant for its lifetime, as the non-coherent loads ask for
+    product = _read("mhc_mx4.cu")
+    product = product[product.index("struct ProductArgs"):product.index("cudaError_t launch_premap_fwd_mx4")]
+    for word in ("ld.global.nc", "__ldg", "load_maps", "load16", "__restrict__"):
+        assert word not in product, word
