@@ -703,11 +703,7 @@ cudaError_t product(const uint8_t* A, const uint8_t* W, ProductArgs p, cudaStrea
     if (!code_map(&mapW, W, p.N, p.K, kChan) || !code_map(&mapA, A, p.T, p.K, S::kTok)) return cudaErrorInvalidValue;
 
     const int sms = device_sm_count(), pairs = (p.K + 511) / 512;
-    int ranks = 1;
-    if (S::kSplit)  // CTAs that share a tile: as many as still fit the GPU, and have work
-        while (ranks < 8 && (ranks + 1) * tiles <= sms && ranks < pairs) ++ranks;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(S::kSplit ? tiles * ranks : tiles < sms ? tiles : sms));
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmemBytes;
     cfg.stream = s;
@@ -715,10 +711,41 @@ cudaError_t product(const uint8_t* A, const uint8_t* W, ProductArgs p, cudaStrea
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)ranks;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = S::kSplit ? 2 : 1;
+    const auto set_ranks = [&](int ranks) {
+        cfg.gridDim = dim3((unsigned)(S::kSplit ? tiles * ranks : tiles < sms ? tiles : sms));
+        attr[1].val.clusterDim.x = (unsigned)ranks;
+    };
+    int ranks = 1;
+    if (S::kSplit) {
+        // CTAs that share a tile: as many as have work, up to 8, while all tiles'
+        // clusters fit the GPU at once.  Its SMs do not say how many do: a cluster
+        // lies within one GPC (of the B200's 148 SMs, 45 clusters of 3 find room, 26
+        // of 5, 15 of 8), so the runtime is asked, once for a size.  With two waves
+        // of clusters one token, N = 2048, K = 4096 takes 9.1 us in clusters of 8,
+        // in one wave 5.6 in clusters of 6; N = 6144 11.5 in 3 and 6.9 in 2.
+        static std::atomic<int> at_once[64][9];  // clusters of that size and one more; 0: not asked
+        for (int r = (int)(pairs < 8 ? pairs : 8); r > 1; --r) {
+            if (r * tiles > sms) continue;
+            set_ranks(r);
+            int n = dev < 64 ? at_once[dev][r].load(std::memory_order_relaxed) : 0;
+            if (n == 0) {
+                if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+                    cudaGetLastError();
+                    n = 0;
+                }
+                ++n;
+                if (dev < 64) at_once[dev][r].store(n, std::memory_order_relaxed);
+            }
+            if (n - 1 >= tiles) {
+                ranks = r;
+                break;
+            }
+        }
+    }
+    set_ranks(ranks);
     return cudaLaunchKernelEx(&cfg, kernel, mapW, mapA, p);
 }
 
@@ -729,9 +756,9 @@ using Split64 = ProductShape<64, 6, true>;
 // 4096 x 8192, though its loads of the streams have the least L1 beside four.
 using Whole192 = ProductShape<192, 4, false>;
 
-// The form by size.  Split forms run one wave of clusters, so they are taken
-// while their tiles fit the GPU at once, and the narrowest that holds the
-// tokens: at N = 8192, K = 4096 one token takes 7.9 us in tiles of 16 and
+// The form by size.  Split forms run one wave, in clusters of as many CTAs as
+// that leaves room for, so they are taken while their tiles fit the GPU at once,
+// and the narrowest that holds the tokens: at N = 8192, K = 4096 one token takes 7.9 us in tiles of 16 and
 // 9.2 in tiles of 64; 200 tokens take 17.6 us in tiles of 64 (256 tiles, two
 // waves) and 11.5 whole.
 template <bool kMix, bool kDiag = false>

@@ -438,6 +438,34 @@ def test_serving_layer_runs_together():
         assert (np.abs(to_np64(Y) - ref) <= tol).all()
 
 
+def _product_us(T, N, K, calls=20):
+    """Least time of a product on the device, calls back to back."""
+    a, w = _operands(T, N, K, 85)
+    out = api.mx4_linear(a, w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(calls):
+            api.mx4_linear(a, w, out=out)
+    best = float("inf")
+    for _ in range(20):
+        t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        t0.record()
+        graph.replay()
+        t1.record()
+        t1.synchronize()
+        best = min(best, t0.elapsed_time(t1) / calls * 1e3)
+    del graph
+    return best
+
+
+@pytest.mark.parametrize("T", (1, 16, 64))
+def test_clusters_that_share_a_tile_run_in_one_wave(T):
+    # 32 tiles fit the GPU in clusters of 4; 16 tiles do not in clusters of 8, of
+    # which the GPCs hold fewer than SMs / 8.  Half the work in one wave takes no
+    # longer than all of it, in two waves nearly twice as long: the bound is between
+    assert _product_us(T, 2048, 4096) <= 1.4 * _product_us(T, 4096, 4096)
+
+
 @pytest.mark.parametrize("role", sorted(api.MX4_ROLES))
 @pytest.mark.parametrize("T,N,K", [(3, 264, 2080), (3, 264, 32768), (60, 264, 32768), (1500, 2056, 4128)])
 def test_a_wait_that_runs_out(T, N, K, role):
