@@ -86,8 +86,8 @@ def parse():
                     choices=["newton_fwd", "sinkhorn_fwd", "sinkhorn_bwd", "implicit_bwd", "mix_fwd", "mix_bwd",
                              "proj_mix_fwd", "proj_mix_bwd", "premap_fwd", "mix_post_bwd", "mix_premap_bwd",
                              "newton_fwd_n", "implicit_bwd_n", "composite_gain", "fwd_bwd_mapped",
-                             "mx_pack", "mx_unpack", "mix_fwd_ckpt", "mix_bwd_ckpt", "mix_post_bwd_ckpt",
-                             "mix_premap_bwd_ckpt", "premap_fwd_mx4", "mx4_linear", "mx4_linear_mix"],
+                             "mx_pack", "mx_unpack", "mix_fwd_ckpt", "proj_mix_fwd_ckpt", "mix_bwd_ckpt",
+                             "mix_post_bwd_ckpt", "mix_premap_bwd_ckpt", "premap_fwd_mx4", "mx4_linear", "mx4_linear_mix"],
                     help="run one kernel --reps times on one case (for ncu) and exit")
     ap.add_argument("--method", default="newton", help="--profile newton_fwd: projection method")
     ap.add_argument("--layout", default="auto", choices=["auto", "thread", "lane_pair", "row_group"],
@@ -1010,6 +1010,7 @@ def run_profile_case(args):
         fn = {"mx_pack": lambda: api.mx_pack(X, args.format),
               "mx_unpack": lambda: api.mx_unpack(Xq, out=Y),
               "mix_fwd_ckpt": lambda: api.residual_mix_fwd_ckpt(X, H, h, F, args.format, out=Y),
+              "proj_mix_fwd_ckpt": lambda: api.proj_mix_fwd_ckpt(lg, h, X, F, args.format, out=Y),
               "mix_bwd_ckpt": lambda: api.residual_mix_bwd_ckpt(Xq, H, h, Fq, dY, need_dlogits=True),
               "mix_post_bwd_ckpt": lambda: api.mix_post_bwd_ckpt(dY, Fq, h),
               "mix_premap_bwd_ckpt": lambda: api.mix_premap_bwd_ckpt(Xq, H, hpre, dY, dx_in),
