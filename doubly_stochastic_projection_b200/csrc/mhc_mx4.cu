@@ -106,11 +106,17 @@ premap_fwd_mx4_kernel(const uint4* X, const float* hpre, uint8_t* codes, uint8_t
 // would be 65 us; operands, scales and outputs share the path between L2 and the
 // SMs); 200 tokens, N = 4104, K = 4096 9.3 us; one token, N = 8192, K = 7168
 // 9.8 us (3.2 TB/s, latency: the launch, the first bytes of memory and the
-// cluster's sum).  With the mix: 16384 tokens, C = 4096, K = 8192 322 to 325 us.
+// cluster's sum).  With the mix: 16384 tokens, C = 4096, K = 8192 322 to 333 us by
+// the GPU; 280 without the loads of the streams, 291 without the stores of Y, 256
+// without both.  An SM has the loads of 32 tokens in flight, between two barriers
+// of the epilogue, so their latency shows.
 //
-// Every wait is bounded (tc5.cuh).  One that runs out, which no valid call
-// does, sets mx4_wait_expired, makes the other roles give up too, and leaves
-// NaN in the outputs that are not done.
+// Every wait at an mbarrier is bounded, by the device's clock (tc5.cuh).  One that
+// runs out, as it does when a role of the CTA fails or the process is switched out
+// for the whole limit, sets mx4_wait_expired, makes the other roles give up too,
+// and leaves NaN in the outputs that are not done.  Not bounded are what all
+// CTAs of a launch come to: the end of the grid before this one, tensor memory
+// (held by no other CTA of this kernel on the SM) and the barriers of a cluster.
 
 constexpr int kChan = 128;      // channels of a tile
 constexpr int kRowBytes = 128;  // of K of a tile: 256 elements
@@ -206,12 +212,9 @@ __device__ __forceinline__ uint32_t scales_within(uint32_t word, int w, int KB)
     return left >= 4 ? word : left <= 0 ? 0u : word & (0xffffffffu >> (8 * (4 - left)));
 }
 
-// What the output of eight channels of a token (vector v of N / 8) takes beside
-// the product: nothing, or the mix's streams and maps, loaded ahead.
 // Two floats in one register pair.  The mix's 160 multiply-adds for a token and
-// vector, two channels an instruction: each rounds as fmaf does, and 16384 x
-// 4096 x 8192 takes 321 us instead of 327 timed in turn, 1000 tokens 40 instead of
-// 42, the epilogue's eight warps being bound by what they issue.
+// vector, two channels an instruction: each rounds as fmaf does, and timed in turn
+// 16384 x 4096 x 8192 takes 333 us instead of 341, 1000 tokens 40 instead of 42.
 __device__ __forceinline__ uint64_t two(float lo, float hi)
 {
     uint64_t d;
@@ -231,6 +234,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return d;
 }
 
+// What the output of eight channels of a token (vector v of N / 8) takes beside
+// the product: nothing, or the mix's streams and maps, loaded ahead.
 template <bool kMix>
 struct StreamVec {
     __device__ __forceinline__ void load(const ProductArgs&, int64_t, int) {}
@@ -760,7 +765,10 @@ using Whole192 = ProductShape<192, 4, false>;
 // that leaves room for, so they are taken while their tiles fit the GPU at once,
 // and the narrowest that holds the tokens: at N = 8192, K = 4096 one token takes 7.9 us in tiles of 16 and
 // 9.2 in tiles of 64; 200 tokens take 17.6 us in tiles of 64 (256 tiles, two
-// waves) and 11.5 whole.
+// waves) and 11.5 whole.  Past one wave the whole form is taken whatever the
+// tokens.  For one token and N = 36864 it is the faster one with K = 1024 (10.9 us,
+// 11.5 in waves of tiles of 16) but not with K = 4096 (36 and 21) or 7168 (51 and
+// 30); from N = 18952 on, that is left.
 template <bool kMix, bool kDiag = false>
 cudaError_t product_by_size(const uint8_t* A, const uint8_t* W, const ProductArgs& p, cudaStream_t s)
 {

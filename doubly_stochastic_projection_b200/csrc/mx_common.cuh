@@ -6,8 +6,10 @@
 // does not pass the format's largest value, so nothing saturates (one case
 // aside, below) and, the scale being a power of two, the division is exact and
 // the only rounding is that of the element itself, to nearest, ties to even:
-// half a step, i.e. 2^-7 of the block's binade for int8, 2^-4 of the value
-// for e4m3 (2^-10 of the binade below its normal range) and 2^-2 for e2m1.
+// half a step, i.e. 2^-7 of the scale for int8; for e4m3 2^-4 of the value, or
+// 2^-10 of the scale below its normal range (2^-6 of the scale); for e2m1 2^-2 of
+// the value, or 2^-2 of the scale below 1 times the scale, where a small value
+// may round to zero.
 // The codes therefore depend on the input alone, not on the order or
 // precision of the arithmetic.
 //
@@ -68,7 +70,9 @@ template <int kFmt>
 __device__ __forceinline__ int mx_scale_byte(uint32_t amax_bits)
 {
     if (amax_bits >= 0x7f800000u) return kMxScaleNaN;
-    if (amax_bits < 0x00800000u) return 0;  // subnormal: below 2 * 2^-127, which every format holds
+    // subnormal: below 2 * 2^-127, which e4m3 and e2m1 hold; int8 holds 127/64 *
+    // 2^-127, the largest subnormal bf16, and is given bf16 only
+    if (amax_bits < 0x00800000u) return 0;
     const int e = (int)((amax_bits + (0x7fffffu - MxFormat<kFmt>::kTopMantissa)) >> 23) - MxFormat<kFmt>::kEmax;
     return min(max(e, 0), 254);
 }

@@ -19,9 +19,11 @@
  *  - All tensor pointers are DEVICE pointers owned by the caller (the one
  *    exception, mhc_birkhoff_fwd_bwd_host, also takes pinned host buffers).
  *    The library allocates no memory, frees nothing and keeps no state
- *    between calls apart from a per-device cache of the SM count and of kernel
- *    attributes, and the two copy streams (with their events) of
- *    mhc_birkhoff_fwd_bwd_host.
+ *    between calls apart from per-device caches (the SM count, kernel attributes
+ *    and occupancy), the address of a driver function, the two copy streams (with
+ *    their events) of mhc_birkhoff_fwd_bwd_host, and a word on each device that
+ *    says that a bounded wait has run out, which mhc_wait_status reads and clears
+ *    for all of the process's streams and threads.
  *  - Every call is asynchronous on `stream` (a cudaStream_t passed as void*;
  *    NULL means the legacy default stream) and returns as soon as the work is
  *    enqueued.
@@ -476,9 +478,10 @@ MHC_API int mhc_mx4_linear_mix(const uint8_t *A_codes, const uint8_t *A_scales, 
 
 /*
  * mhc_wait_status -- diagnostic of the products: their kernels hand tiles from
- * one warp to another through waits that end after two seconds at most.  A
- * wait that runs out means a fault of the device or a defect, not a bad
- * argument; the outputs that were not done are NaN.  Returns MHC_ERR_WAIT if
+ * one warp to another through waits that end after two seconds at most, by the
+ * device's clock, which also runs while the process is switched out.  A wait that
+ * runs out means that, a fault of the device or a defect, not a bad argument; the
+ * outputs that were not done are NaN.  Returns MHC_ERR_WAIT if
  * that happened on the current device since the last call, MHC_ERR_CUDA if the
  * device cannot be asked, MHC_OK otherwise.  Synchronises the device: not for
  * use during stream capture.
