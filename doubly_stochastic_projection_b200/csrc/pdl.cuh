@@ -16,9 +16,9 @@
 // forward + backward step 24.9 us against 19.7 us (20.8 us without).  The
 // kernels that write the 4-bit product's operand do release it at their start
 // (pdl_release): its CTAs set up barriers, tensor memory and clusters for some
-// 2 us before they wait.  Read map and product, one token: 11.1 us against
-// 12.1 at 8192 x 7168, 6.4 against 7.1 at 4104 x 4096; 8192 tokens 152.8
-// against 153.6.  All CTAs of such a kernel run at once (a persistent grid), so
+// 2 us before they wait.  Read map and product, one token: 11.0 us against
+// 12.0 at 8192 x 7168, 6.2 against 7.0 at 4104 x 4096; 200 tokens there 11.5
+// against 12.3; 8192 tokens of 8192 x 4096 161.5 either way.  All CTAs of such a kernel run at once (a persistent grid), so
 // what is released takes no place that they still need.
 #pragma once
 

@@ -80,3 +80,13 @@ def test_measured_peaks_reader(tmp_path):
     f.write_text(json.dumps({"bf16_tflops": 1590}))
     assert bench.measured_peaks(str(f)) == (bench.FALLBACK_HBM_GBS, "fallback")
     assert bench.measured_peaks(str(tmp_path / "absent.json")) == (bench.FALLBACK_HBM_GBS, "fallback")
+
+
+def test_committed_traffic_belongs_to_the_present_sources():
+    # the roofline's DRAM traffic is dropped, without a word, when the projection
+    # kernels' sources or the headers they are built from have changed since
+    if ROOT not in sys.path:
+        sys.path.insert(0, ROOT)
+    import bench
+    for kernel in ("newton_fwd_kernel", "implicit_bwd_kernel"):
+        assert bench.profiled_traffic(kernel) is not None, "capture profiles/traffic.json again"
