@@ -25,8 +25,9 @@ copies, pipelined, inside the timed region), the roofline of the dominant kernel
 against the measured HBM copy bandwidth and the FP32 and MUFU issue peaks, the
 fp64 CPU oracle timed on the host cores, SM clocks through NVML, and (unless
 --no-extras) the 1M/4M/16M sweep, 20-iteration Sinkhorn, the layouts of the
-Newton forward, and the residual-mix workloads.  The last key of the JSON line
-is a compact ``targets`` summary of the fractions the extras measured.
+Newton forward, and the residual-mix workloads, as a JSON object on stderr.
+The last key of the JSON line is a compact ``targets`` summary of the fractions
+the extras measured.
 
 ``--impl reference`` times the fp64 CPU oracle (the reference implementation
 of what the kernels compute) on bounded samples of the same workload.
@@ -486,6 +487,16 @@ def projection_roofline(kname, n, t, hbm, mhz, its_mean=None, polished=None):
     return bound, roofs
 
 
+def emit(line):
+    """Prints the one JSON line.  The extras are an object of their own on stderr:
+    with them the line is 22 KB, and what keeps only the end of the output, as the
+    tail of a log does, loses the headline."""
+    extra = line.pop("extras", None)
+    if extra is not None:
+        print(json.dumps({"extras": extra}), file=sys.stderr, flush=True)
+    print(json.dumps(line), flush=True)
+
+
 # ----------------------------------------------------------------- extras
 
 
@@ -924,7 +935,7 @@ def run_b200(args):
     line["targets"] = targets_summary(line, hbm)
 
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        emit(line)
     if pg is not None:
         barrier(pg, dev)
         pg.destroy_process_group()

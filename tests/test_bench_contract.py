@@ -90,3 +90,18 @@ def test_committed_traffic_belongs_to_the_present_sources():
     import bench
     for kernel in ("newton_fwd_kernel", "implicit_bwd_kernel"):
         assert bench.profiled_traffic(kernel) is not None, "capture profiles/traffic.json again"
+
+
+def test_the_line_is_short_whatever_the_extras(capsys):
+    # readers keep the end of the output; the headline is at the line's beginning
+    if ROOT not in sys.path:
+        sys.path.insert(0, ROOT)
+    import bench
+    line = {"metric": bench.METRIC, "value": 1.0, "config": bench.headline_config(1),
+            "extras": {"sweep": [{"n": i, "rate": i / 3.0} for i in range(2000)]}, "targets": {"frac": 0.5}}
+    bench.emit(dict(line))
+    out, err = capsys.readouterr()
+    assert len(out.splitlines()) == 1 and len(out) < 8192
+    got = _json_lines(out)[0]
+    assert got == {k: v for k, v in line.items() if k != "extras"}
+    assert _json_lines(err)[0]["extras"] == line["extras"]
