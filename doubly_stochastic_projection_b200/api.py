@@ -742,12 +742,14 @@ def mx4_linear_diag(a: MxTensor, w: MxTensor, wait_ns: int = 2_000_000_000, idle
     """mx4_linear whose waits end after wait_ns nanoseconds, and with roles of its
     kernel (names of MX4_ROLES) left out, for which the others wait in vain: for
     tests of what becomes of a wait that runs out (wait_status)."""
+    if not set(idle) <= set(MX4_ROLES):
+        raise ValueError("idle must be among %s, got %r" % (", ".join(MX4_ROLES), idle))
+    mask = sum({MX4_ROLES[r] for r in idle})
     T, N, K = _product_shapes(a, w)
     if out is None:
         out = a.codes.new_empty((T, N), dtype=torch.bfloat16)
     else:
         _need(out, "out", torch.bfloat16, (T, N))
-    mask = sum({MX4_ROLES[r] for r in idle})
     _launch(lib().mhc_mx4_linear_diag, (a[0], a[1], w[0], w[1], out), T, N, K, int(wait_ns), mask)
     return out
 

@@ -100,3 +100,10 @@ def test_waits_that_run_out_have_a_status_of_their_own(L):
     for k in range(5):
         assert f(*[None if i == k else FAKE for i in range(5)], 4, 64, 64, 1000, 1, None) == NULL
         assert f(*[FAKE + 2 if i == k else FAKE for i in range(5)], 4, 64, 64, 1000, 1, None) == ALIGN
+
+
+def test_roles_that_do_not_exist_are_refused():
+    from doubly_stochastic_projection_b200 import api
+
+    with pytest.raises(ValueError):
+        api.mx4_linear_diag(None, None, idle=("epilogue",))
